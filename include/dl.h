@@ -362,6 +362,127 @@ dl_status dl_block_scores_noalloc(const dl_attn_desc* desc, const void* Q_dec,
                                   const int32_t* q_idx, const int32_t* q_cnt, const float* Kbar,
                                   int n_units, double* score, void* stream);
 
+/* ---- One token at a time over the same cache ----------------------------
+ * (c1)-(c4) serve a sequence that grows token by token in the paged pools
+ * above: the projection of the new tokens becomes queries and cached rows
+ * (c1), the new token attends to what its sequence has cached (c2), and when
+ * a cache outgrows its budget the tokens of least accumulated attention leave
+ * it (c3, c4).  [standard autoregressive decoding and accumulated-attention
+ * cache eviction; the pages cache the long context but do not grow it token
+ * by token]
+ *   - Each sequence has its own length; desc->L_ctx is the capacity in tokens
+ *     that the page table and the per-token arrays have room for.
+ *   - Per-token arrays have one row per decision: n_mass is 1 (one row per
+ *     sequence, shared by its KV heads) or H_kv (one per KV head).
+ *       tok_mass fp32  [batch][n_mass][L_ctx]  accumulated attention weight
+ *       tok_pos  int32 [batch][n_mass][L_ctx]  position in the sequence
+ *     Entries at or behind a sequence's length are neither read nor written.
+ *   - These calls do not keep the pooled keys of dl_pool_keys up to date:
+ *     call dl_pool_keys before the next block selection over this cache.
+ *   - Buffers that a call writes must not overlap any other buffer of the
+ *     call. */
+
+/* (c1) Per-head norm of queries and keys, position rotation, head split and
+ * cache append, in one pass over the projection's output.
+ *   qkv  [batch][n_tok][qkv_stride]: each token's row holds the H query heads,
+ *        the H_kv key heads and the H_kv value heads, d values each, then
+ *        anything (qkv_stride >= (H + 2 H_kv) d elements, rows a multiple of
+ *        16 bytes apart); dtype of the descriptor.
+ * For a query or key head x of the token at position p = pos[b][i]:
+ *   y = x * w / sqrt(mean(x^2) + eps), w = q_weight or k_weight [d] (dtype of
+ *       the descriptor; NULL: y = x);
+ *   for j < rot_dim/2, with a = p * inv_freq[j]:
+ *     (y_u, y_v) <- (y_u cos a - y_v sin a, y_v cos a + y_u sin a),
+ *     (u, v) = (j, j + rot_dim/2), or (2j, 2j+1) when interleaved != 0;
+ * values are only copied.  Computed in fp32 (the angle and its reduction in
+ * fp64, so that far positions keep their phase), rounded once to the dtype.
+ *   pos       int32 [batch][n_tok], any value
+ *   inv_freq  fp32 [rot_dim/2] (NULL when rot_dim is 0); rot_dim a multiple
+ *             of 8, 0..d
+ *   Q_out     [batch][H][n_tok][d]
+ *   K_out, V_out  [batch][H_kv][n_tok][d], both or neither
+ * Cache append (K_pool, V_pool, page_table and start given, or all NULL):
+ * token i of sequence b is written at logical position t = start[b] + i, and
+ * where given tok_pos[b][.][t] = pos[b][i], tok_mass[b][.][t] = 0 and
+ * end[b] = start[b] + n_tok.  A sequence with start[b] < 0 or start[b] + n_tok
+ * > L_ctx is not appended (end[b] = start[b]); a token whose page slot is out
+ * of range is not appended.  Both report DL_ERR_BAD_INDEX.
+ *   start int32 [batch], end int32 [batch] or NULL (not the same buffer)
+ *   n_mass  rows of tok_pos and tok_mass (ignored when both are NULL)
+ * Either the cache or K_out and V_out must be given.  desc->L_q is not used.
+ * Requires 1 <= n_tok, batch * n_tok < 2^31, eps >= 0; 16-byte alignment of
+ * qkv, the weights, Q_out, K_out, V_out and the pools. */
+dl_status dl_qk_norm_rope(const dl_attn_desc* desc, const void* qkv, int64_t qkv_stride, int n_tok,
+                          const int32_t* pos, const void* q_weight, const void* k_weight,
+                          float eps, const float* inv_freq, int rot_dim, int interleaved,
+                          void* Q_out, void* K_out, void* V_out, const int32_t* start,
+                          const int32_t* page_table, void* K_pool, void* V_pool, int32_t* end,
+                          int32_t* tok_pos, float* tok_mass, int n_mass, void* stream);
+
+/* (c2) Attention of one new token per sequence over its cached tokens.
+ * For every query head h (KV head g), over t < n = ctx_len[b]:
+ *   a_t = scale * q_h . k_t,  lse = ln sum_t e^{a_t},
+ *   o_h = sum_t e^{a_t - lse} v_t
+ * fp32 accumulation, O rounded to nearest-even in the input dtype.  The new
+ * token attends to itself when its own key is in the cache (c1 puts it there).
+ * n = 0: O = 0 and lse = -infinity.  A length outside 0..L_ctx counts as 0,
+ * and a page slot out of range makes that sequence's results unspecified;
+ * both report DL_ERR_BAD_INDEX.
+ *   Q        [batch][H][d], O [batch][H][d], 16-byte aligned (desc->L_q == 1)
+ *   ctx_len  int32 [batch]
+ *   lse      fp32 [batch][H] or NULL
+ *   tok_mass NULL, or accumulated in place for t < n:
+ *            mass[b][m][t] = decay * mass[b][m][t] + sum_h e^{a_t - lse_h}
+ *            over the query heads h of KV head m (n_mass == H_kv) or of the
+ *            sequence (n_mass == 1); decay 0 does not read the old value
+ *   n_mass   rows of tok_mass (ignored when it is NULL)
+ * The result does not depend on the grid's timing: partial sums are joined in
+ * a fixed order.  Requires 0 <= decay <= 1. */
+dl_status dl_decode_attn(const dl_attn_desc* desc, const void* Q, const void* K_pool,
+                         const void* V_pool, const int32_t* page_table, const int32_t* ctx_len,
+                         void* O, float* lse, float* tok_mass, int n_mass, float decay, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* (c3) Which cached tokens leave when a budget is kept.  For each decision
+ * row m of a sequence of n = ctx_len[b] tokens with n > budget, `budget`
+ * tokens stay: first the held ones -- tok_pos < n_first, or tok_pos > P -
+ * n_recent with P the row's largest tok_pos -- then those of largest tok_mass
+ * (a held token ranks like a mass of +infinity, a NaN like -infinity; ties ->
+ * lower index).  The cache is closed up by moving kept rows from behind the
+ * budget into the holes before it:
+ *   hole_idx[b][m][i] = the i-th index t < budget that leaves, ascending,
+ *   fill_idx[b][m][i] = the i-th index t >= budget that stays, ascending,
+ * move_cnt[b][m] of each (there are as many), -1 behind them.  n <= budget:
+ * no moves.  new_len[b] = min(n, budget).  Tokens keep no order; tok_pos says
+ * where each was.
+ *   tok_pos  NULL: the index itself is the position
+ *   hole_idx, fill_idx  int32 [batch][n_mass][max_move] (out; may be NULL when
+ *            max_move is 0), max_move >= min(budget, max(L_ctx - budget, 0))
+ *   move_cnt int32 [batch][n_mass] (out)
+ *   new_len  int32 [batch] (out; not the buffer of ctx_len)
+ * A length outside 0..L_ctx reports DL_ERR_BAD_INDEX: no moves, new_len =
+ * ctx_len.  Nothing of the cache is changed.  dl_sink_mass' output is such a
+ * tok_mass with n_mass 1.  Requires budget >= 1, n_first, n_recent >= 0 and
+ * n_first + n_recent <= budget.  Uses batch, H_kv and L_ctx of desc. */
+dl_status dl_evict_select(const dl_attn_desc* desc, const float* tok_mass, const int32_t* tok_pos,
+                          int n_mass, const int32_t* ctx_len, int budget, int n_first,
+                          int n_recent, int32_t* hole_idx, int32_t* fill_idx, int max_move,
+                          int32_t* move_cnt, int32_t* new_len, void* stream);
+
+/* (c4) The moves of an eviction plan: for i < move_cnt[b][m], the K and V rows
+ * at logical position fill_idx[b][m][i] are copied to hole_idx[b][m][i], for
+ * KV head m (n_mass == H_kv) or for every KV head (n_mass == 1), and tok_pos
+ * and tok_mass entries (each may be NULL) with them.  Rows behind the budget
+ * are left as they were.  The lists are those of dl_evict_select, or any whose
+ * holes are distinct and are no fills (otherwise which move wins is
+ * unspecified).  A move whose index is outside 0..L_ctx-1 or whose page slot
+ * is out of range is skipped, a count outside 0..max_move is clamped; both
+ * report DL_ERR_BAD_INDEX.  Pages must not be shared between sequences. */
+dl_status dl_cache_compact(const dl_attn_desc* desc, const int32_t* hole_idx,
+                           const int32_t* fill_idx, const int32_t* move_cnt, int max_move,
+                           int n_mass, const int32_t* page_table, void* K_pool, void* V_pool,
+                           int32_t* tok_pos, float* tok_mass, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

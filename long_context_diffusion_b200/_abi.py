@@ -71,6 +71,15 @@ _SIGS = {
                                  _vp], _c_int),
     "dl_sparse_attn_gather": ([ctypes.POINTER(dl_attn_desc), _vp, _vp, _vp, _vp, _vp, _vp,
                                _c_int, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], _c_int),
+    "dl_qk_norm_rope": ([ctypes.POINTER(dl_attn_desc), _vp, ctypes.c_int64, _c_int, _vp, _vp, _vp,
+                         ctypes.c_float, _vp, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                         _vp, _vp, _vp, _c_int, _vp], _c_int),
+    "dl_decode_attn": ([ctypes.POINTER(dl_attn_desc), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                        _c_int, ctypes.c_float, _vp, ctypes.c_size_t, _vp], _c_int),
+    "dl_evict_select": ([ctypes.POINTER(dl_attn_desc), _vp, _vp, _c_int, _vp, _c_int, _c_int,
+                         _c_int, _vp, _vp, _c_int, _vp, _vp, _vp], _c_int),
+    "dl_cache_compact": ([ctypes.POINTER(dl_attn_desc), _vp, _vp, _vp, _c_int, _c_int, _vp, _vp,
+                          _vp, _vp, _vp, _vp], _c_int),
 }
 
 
@@ -248,3 +257,129 @@ def dl_block_scores_noalloc(desc, Q_dec, q_idx, q_cnt, Kbar, n_units, score, str
     device memory; the library's built-in 32 MiB scratch array is used."""
     _check(lib.dl_block_scores_noalloc(ctypes.byref(desc), _p(Q_dec), _p(q_idx), _p(q_cnt),
                                        _p(Kbar), n_units, _p(score), _s(stream)))
+
+
+# ---- one token at a time over the same cache (dl.h, c1-c4) ----
+
+class _Buffers:
+    """Buffer checks of one call: every tensor contiguous, of the stated type
+    and number of elements, all on one device, which must be the current one
+    (the call launches there).  Returns the data pointers."""
+
+    def __init__(self, name: str):
+        self.name, self.dev = name, torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+    def __call__(self, t, what: str, dtype, n: int):
+        if t is None:
+            return None
+        if t.dtype is not dtype or t.numel() != n or t.get_device() != self.dev or \
+                self.dev < 0 or not t.is_contiguous():
+            raise ValueError(
+                f"{self.name}: {what} must be a contiguous {dtype} tensor of {n} elements on the "
+                f"current CUDA device ({self.dev}), got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+
+def _dtype_of(desc):
+    return torch.bfloat16 if desc.dtype == DL_BF16 else torch.float32
+
+
+def _mass_rows(name, desc, *arrays):
+    """Rows per sequence of the per-token arrays [batch][n_mass][...]."""
+    for t in arrays:
+        if t is not None:
+            if t.dim() != 3:
+                raise ValueError(f"{name}: per-token arrays are [batch][n_mass][...], got "
+                                 f"{tuple(t.shape)}")
+            return t.shape[1]
+    return 1
+
+
+def dl_qk_norm_rope(desc, qkv, pos, q_weight, k_weight, eps, inv_freq, Q_out, K_out=None,
+                    V_out=None, start=None, page_table=None, K_pool=None, V_pool=None, end=None,
+                    tok_pos=None, tok_mass=None, interleaved=False, stream=None):
+    """qkv [batch][n_tok][>= (H + 2 H_kv) d], possibly a view whose tokens are
+    further apart (unit stride inside a token, equal steps between tokens).
+    inv_freq None: no rotation.  Outputs: Q_out, and K_out/V_out and/or the
+    cache (start, page_table, K_pool, V_pool, with end, tok_pos, tok_mass)."""
+    B, H, H_kv, d = desc.batch, desc.H, desc.H_kv, desc.d
+    name, dt, buf = "dl_qk_norm_rope", _dtype_of(desc), _Buffers("dl_qk_norm_rope")
+    if qkv.dim() != 3 or qkv.shape[0] != B or qkv.dtype is not dt or \
+            qkv.get_device() != buf.dev or buf.dev < 0:
+        raise ValueError(f"{name}: qkv must be a [{B}][n_tok][...] {dt} tensor on the current CUDA "
+                         f"device, got {qkv.dtype} {tuple(qkv.shape)} on {qkv.device}")
+    n = qkv.shape[1]
+    s0, stride, s2 = qkv.stride()
+    if n == 1:
+        stride = s0 if B > 1 else max(stride, qkv.shape[2])
+    if s2 != 1 or (B > 1 and n > 1 and s0 != n * stride) or stride < qkv.shape[2] or \
+            qkv.shape[2] < (H + 2 * H_kv) * d:
+        raise ValueError(f"{name}: qkv rows must hold (H + 2 H_kv) d = {(H + 2 * H_kv) * d} values "
+                         f"with unit stride and equal steps between tokens, got shape "
+                         f"{tuple(qkv.shape)} strides {qkv.stride()}")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    n_mass = _mass_rows(name, desc, tok_pos, tok_mass)
+    rows, pool, book = B * n * d, desc.n_slots * H_kv * desc.page * d, B * n_mass * desc.L_ctx
+    i32, f32 = torch.int32, torch.float32
+    _check(lib.dl_qk_norm_rope(
+        ctypes.byref(desc), qkv.data_ptr(), stride, n, buf(pos, "pos", i32, B * n),
+        buf(q_weight, "q_weight", dt, d), buf(k_weight, "k_weight", dt, d), eps,
+        buf(inv_freq, "inv_freq", f32, rot // 2), rot, interleaved,
+        buf(Q_out, "Q_out", dt, rows * H), buf(K_out, "K_out", dt, rows * H_kv),
+        buf(V_out, "V_out", dt, rows * H_kv), buf(start, "start", i32, B),
+        buf(page_table, "page_table", i32, B * desc.n_pages), buf(K_pool, "K_pool", dt, pool),
+        buf(V_pool, "V_pool", dt, pool), buf(end, "end", i32, B),
+        buf(tok_pos, "tok_pos", i32, book), buf(tok_mass, "tok_mass", f32, book), n_mass,
+        _s(stream)))
+
+
+def dl_decode_attn(desc, Q, K_pool, V_pool, page_table, ctx_len, O, lse, ws, tok_mass=None,
+                   decay=1.0, stream=None):
+    """tok_mass [batch][1 or H_kv][L_ctx], accumulated in place (or None)."""
+    B, H, d = desc.batch, desc.H, desc.d
+    name, dt, buf = "dl_decode_attn", _dtype_of(desc), _Buffers("dl_decode_attn")
+    n_mass = _mass_rows(name, desc, tok_mass)
+    pool = desc.n_slots * desc.H_kv * desc.page * d
+    if ws.get_device() != buf.dev or not ws.is_contiguous():
+        raise ValueError(f"{name}: the workspace must be contiguous on the current CUDA device")
+    _check(lib.dl_decode_attn(
+        ctypes.byref(desc), buf(Q, "Q", dt, B * H * d), buf(K_pool, "K_pool", dt, pool),
+        buf(V_pool, "V_pool", dt, pool),
+        buf(page_table, "page_table", torch.int32, B * desc.n_pages),
+        buf(ctx_len, "ctx_len", torch.int32, B), buf(O, "O", dt, B * H * d),
+        buf(lse, "lse", torch.float32, B * H),
+        buf(tok_mass, "tok_mass", torch.float32, B * n_mass * desc.L_ctx), n_mass, decay,
+        ws.data_ptr(), ws.numel() * ws.element_size(), _s(stream)))
+
+
+def dl_evict_select(desc, tok_mass, tok_pos, ctx_len, budget, n_first, n_recent, hole_idx,
+                    fill_idx, move_cnt, new_len, stream=None):
+    """hole_idx, fill_idx [batch][n_mass][max_move]; tok_pos may be None (the
+    index is the position)."""
+    B, name, buf = desc.batch, "dl_evict_select", _Buffers("dl_evict_select")
+    n_mass = _mass_rows(name, desc, tok_mass)
+    max_move = 0 if hole_idx is None else hole_idx.shape[-1]
+    book, moves, i32 = B * n_mass * desc.L_ctx, B * n_mass * max_move, torch.int32
+    _check(lib.dl_evict_select(
+        ctypes.byref(desc), buf(tok_mass, "tok_mass", torch.float32, book),
+        buf(tok_pos, "tok_pos", i32, book), n_mass, buf(ctx_len, "ctx_len", i32, B), budget,
+        n_first, n_recent, buf(hole_idx, "hole_idx", i32, moves),
+        buf(fill_idx, "fill_idx", i32, moves), max_move,
+        buf(move_cnt, "move_cnt", i32, B * n_mass), buf(new_len, "new_len", i32, B), _s(stream)))
+
+
+def dl_cache_compact(desc, hole_idx, fill_idx, move_cnt, page_table, K_pool, V_pool, tok_pos=None,
+                     tok_mass=None, stream=None):
+    """The moves of dl_evict_select's lists ([batch][n_mass][max_move])."""
+    B, name, buf = desc.batch, "dl_cache_compact", _Buffers("dl_cache_compact")
+    n_mass = _mass_rows(name, desc, hole_idx)
+    max_move, dt, i32 = hole_idx.shape[-1], _dtype_of(desc), torch.int32
+    pool = desc.n_slots * desc.H_kv * desc.page * desc.d
+    book, moves = B * n_mass * desc.L_ctx, B * n_mass * max_move
+    _check(lib.dl_cache_compact(
+        ctypes.byref(desc), buf(hole_idx, "hole_idx", i32, moves),
+        buf(fill_idx, "fill_idx", i32, moves), buf(move_cnt, "move_cnt", i32, B * n_mass), max_move,
+        n_mass, buf(page_table, "page_table", i32, B * desc.n_pages),
+        buf(K_pool, "K_pool", dt, pool), buf(V_pool, "V_pool", dt, pool),
+        buf(tok_pos, "tok_pos", i32, book), buf(tok_mass, "tok_mass", torch.float32, book),
+        _s(stream)))

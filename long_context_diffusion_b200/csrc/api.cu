@@ -122,7 +122,7 @@ unsigned kernel_flags() { return g_kernel_flags.load(std::memory_order_relaxed);
 
 extern "C" {
 
-int dl_version(void) { return 200; }
+int dl_version(void) { return 300; }
 
 unsigned dl_set_kernel_flags(unsigned flags) { return g_kernel_flags.exchange(flags); }
 
@@ -165,6 +165,10 @@ dl_status dl_workspace_size(const dl_attn_desc* desc, size_t* bytes) {
   need = x > need ? x : need;
   x = dl::sinks_workspace(s);
   need = x > need ? x : need;
+  if (s.L_q == 1) {  // the only descriptors dl_decode_attn takes
+    x = dl::decode_workspace(s);
+    need = x > need ? x : need;
+  }
   *bytes = need;
   return ok();
 }
@@ -424,6 +428,139 @@ dl_status dl_token_select(const dl_attn_desc* desc, const void* Q_dec, const voi
                                           chunk_stride, chunk_content, topT, Kexp, tok_pos,
                                           tok_cnt, err, as_stream(stream)),
                   "dl_token_select launch");
+}
+
+// Per-token arrays have one row per sequence or one per KV head.
+static bool mass_rows_ok(const dl::Shape& s, int n_mass) { return n_mass == 1 || n_mass == s.H_kv; }
+
+dl_status dl_qk_norm_rope(const dl_attn_desc* desc, const void* qkv, int64_t qkv_stride, int n_tok,
+                          const int32_t* pos, const void* q_weight, const void* k_weight,
+                          float eps, const float* inv_freq, int rot_dim, int interleaved,
+                          void* Q_out, void* K_out, void* V_out, const int32_t* start,
+                          const int32_t* page_table, void* K_pool, void* V_pool, int32_t* end,
+                          int32_t* tok_pos, float* tok_mass, int n_mass, void* stream) {
+  dl::Shape s;
+  dl_status st = check_desc(desc, &s);
+  if (st != DL_OK) return st;
+  if (!qkv || !pos || !Q_out || (rot_dim != 0 && !inv_freq))
+    return fail(DL_ERR_INVALID_ARG, "dl_qk_norm_rope: NULL pointer");
+  if ((K_out == nullptr) != (V_out == nullptr))
+    return fail(DL_ERR_INVALID_ARG, "dl_qk_norm_rope: K_out and V_out go together");
+  const bool cache = start != nullptr;
+  if ((page_table != nullptr) != cache || (K_pool != nullptr) != cache || (V_pool != nullptr) != cache)
+    return fail(DL_ERR_INVALID_ARG, "dl_qk_norm_rope: start, page_table, K_pool and V_pool go together");
+  if (!cache && (end || tok_pos || tok_mass))
+    return fail(DL_ERR_INVALID_ARG, "dl_qk_norm_rope: end, tok_pos and tok_mass need the cache");
+  if (!cache && !K_out)
+    return fail(DL_ERR_INVALID_ARG, "dl_qk_norm_rope: neither the cache nor K_out and V_out given");
+  if (cache && end == start)
+    return fail(DL_ERR_INVALID_ARG, "dl_qk_norm_rope: end and start are the same buffer");
+  if ((tok_pos || tok_mass) && !mass_rows_ok(s, n_mass))
+    return fail(DL_ERR_INVALID_ARG, "n_mass=%d (need 1 or H_kv=%d)", n_mass, s.H_kv);
+  if (n_tok < 1 || (long long)s.batch * n_tok >= (1ll << 31))
+    return fail(DL_ERR_INVALID_ARG, "n_tok=%d (need >= 1, batch * n_tok < 2^31)", n_tok);
+  if (!(eps >= 0.0f) || std::isinf(eps)) return fail(DL_ERR_INVALID_ARG, "eps=%g", (double)eps);
+  if (rot_dim < 0 || rot_dim > s.d) return fail(DL_ERR_INVALID_ARG, "rot_dim=%d (need 0..d)", rot_dim);
+  if (rot_dim % 8 != 0)
+    return fail(DL_ERR_UNSUPPORTED, "rot_dim=%d (need a multiple of 8)", rot_dim);
+  const int64_t need = (int64_t)(s.H + 2 * s.H_kv) * s.d;
+  if (qkv_stride < need || qkv_stride > (1ll << 32))
+    return fail(DL_ERR_INVALID_ARG, "qkv_stride=%lld (need >= %lld)", (long long)qkv_stride,
+                (long long)need);
+  if (qkv_stride * (s.dtype == DL_BF16 ? 2 : 4) % 16 != 0)
+    return fail(DL_ERR_INVALID_ARG, "qkv_stride=%lld: rows not 16-byte aligned",
+                (long long)qkv_stride);
+  if (!aligned16(qkv) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(Q_out) ||
+      !aligned16(K_out) || !aligned16(V_out) || !aligned16(K_pool) || !aligned16(V_pool))
+    return fail(DL_ERR_INVALID_ARG, "dl_qk_norm_rope: buffers must be 16-byte aligned");
+  unsigned* err = nullptr;
+  if ((st = error_word(&err)) != DL_OK) return st;
+  dl::RopeArgs a{};
+  a.s = s; a.qkv = qkv; a.qkv_stride = qkv_stride; a.n_tok = n_tok; a.pos = pos;
+  a.q_weight = q_weight; a.k_weight = k_weight; a.eps = eps; a.inv_freq = inv_freq;
+  a.rot_dim = rot_dim; a.interleaved = interleaved != 0; a.Q_out = Q_out; a.K_out = K_out;
+  a.V_out = V_out; a.start = start; a.page_table = page_table; a.K_pool = K_pool;
+  a.V_pool = V_pool; a.end = end; a.tok_pos = tok_pos; a.tok_mass = tok_mass;
+  a.n_mass = (tok_pos || tok_mass) ? n_mass : 0; a.err = err;
+  return launched(dl::launch_qk_norm_rope(a, as_stream(stream)), "dl_qk_norm_rope launch");
+}
+
+dl_status dl_decode_attn(const dl_attn_desc* desc, const void* Q, const void* K_pool,
+                         const void* V_pool, const int32_t* page_table, const int32_t* ctx_len,
+                         void* O, float* lse, float* tok_mass, int n_mass, float decay, void* ws,
+                         size_t ws_bytes, void* stream) {
+  dl::Shape s;
+  dl_status st = check_desc(desc, &s);
+  if (st != DL_OK) return st;
+  if (s.L_q != 1) return fail(DL_ERR_UNSUPPORTED, "dl_decode_attn: L_q=%d (need 1)", s.L_q);
+  if (!Q || !K_pool || !V_pool || (!page_table && s.n_pages > 0) || !ctx_len || !O)
+    return fail(DL_ERR_INVALID_ARG, "dl_decode_attn: NULL pointer");
+  if (!aligned16(Q) || !aligned16(K_pool) || !aligned16(V_pool) || !aligned16(O))
+    return fail(DL_ERR_INVALID_ARG, "dl_decode_attn: Q/K/V/O pointers must be 16-byte aligned");
+  if (tok_mass && !mass_rows_ok(s, n_mass))
+    return fail(DL_ERR_INVALID_ARG, "n_mass=%d (need 1 or H_kv=%d)", n_mass, s.H_kv);
+  if (tok_mass && !(decay >= 0.0f && decay <= 1.0f))
+    return fail(DL_ERR_INVALID_ARG, "decay=%g (need 0..1)", (double)decay);
+  if ((st = need_ws(ws, ws_bytes, dl::decode_workspace(s))) != DL_OK) return st;
+  unsigned* err = nullptr;
+  if ((st = error_word(&err)) != DL_OK) return st;
+  dl::DecodeArgs a{};
+  a.s = s; a.Q = Q; a.Kp = K_pool; a.Vp = V_pool; a.page_table = page_table; a.ctx_len = ctx_len;
+  a.O = O; a.lse = lse; a.tok_mass = tok_mass; a.n_mass = tok_mass ? n_mass : 0; a.decay = decay;
+  a.ws = ws; a.err = err;
+  return launched(dl::launch_decode_attn(a, as_stream(stream)), "dl_decode_attn launch");
+}
+
+dl_status dl_evict_select(const dl_attn_desc* desc, const float* tok_mass, const int32_t* tok_pos,
+                          int n_mass, const int32_t* ctx_len, int budget, int n_first,
+                          int n_recent, int32_t* hole_idx, int32_t* fill_idx, int max_move,
+                          int32_t* move_cnt, int32_t* new_len, void* stream) {
+  dl::Shape s;
+  dl_status st = check_desc(desc, &s);
+  if (st != DL_OK) return st;
+  if (!tok_mass || !ctx_len || !move_cnt || !new_len || (max_move > 0 && (!hole_idx || !fill_idx)))
+    return fail(DL_ERR_INVALID_ARG, "dl_evict_select: NULL pointer");
+  if (new_len == ctx_len)
+    return fail(DL_ERR_INVALID_ARG, "dl_evict_select: new_len and ctx_len are the same buffer");
+  if (!mass_rows_ok(s, n_mass))
+    return fail(DL_ERR_INVALID_ARG, "n_mass=%d (need 1 or H_kv=%d)", n_mass, s.H_kv);
+  if (budget < 1 || n_first < 0 || n_recent < 0 || (long long)n_first + n_recent > budget)
+    return fail(DL_ERR_INVALID_ARG, "budget=%d n_first=%d n_recent=%d", budget, n_first, n_recent);
+  const int spare = s.L_ctx > budget ? s.L_ctx - budget : 0;
+  const int most = spare < budget ? spare : budget;
+  if (max_move < most)
+    return fail(DL_ERR_INVALID_ARG, "max_move=%d < min(budget, L_ctx - budget) = %d", max_move, most);
+  unsigned* err = nullptr;
+  if ((st = error_word(&err)) != DL_OK) return st;
+  dl::EvictArgs a{};
+  a.s = s; a.tok_mass = tok_mass; a.tok_pos = tok_pos; a.n_mass = n_mass; a.ctx_len = ctx_len;
+  a.budget = budget; a.n_first = n_first; a.n_recent = n_recent; a.hole_idx = hole_idx;
+  a.fill_idx = fill_idx; a.max_move = max_move; a.move_cnt = move_cnt; a.new_len = new_len;
+  a.err = err;
+  return launched(dl::launch_evict_select(a, as_stream(stream)), "dl_evict_select launch");
+}
+
+dl_status dl_cache_compact(const dl_attn_desc* desc, const int32_t* hole_idx,
+                           const int32_t* fill_idx, const int32_t* move_cnt, int max_move,
+                           int n_mass, const int32_t* page_table, void* K_pool, void* V_pool,
+                           int32_t* tok_pos, float* tok_mass, void* stream) {
+  dl::Shape s;
+  dl_status st = check_desc(desc, &s);
+  if (st != DL_OK) return st;
+  if (max_move < 0) return fail(DL_ERR_INVALID_ARG, "max_move=%d", max_move);
+  if (!move_cnt || !page_table || !K_pool || !V_pool || (max_move > 0 && (!hole_idx || !fill_idx)))
+    return fail(DL_ERR_INVALID_ARG, "dl_cache_compact: NULL pointer");
+  if (!aligned16(K_pool) || !aligned16(V_pool))
+    return fail(DL_ERR_INVALID_ARG, "dl_cache_compact: pools must be 16-byte aligned");
+  if (!mass_rows_ok(s, n_mass))
+    return fail(DL_ERR_INVALID_ARG, "n_mass=%d (need 1 or H_kv=%d)", n_mass, s.H_kv);
+  unsigned* err = nullptr;
+  if ((st = error_word(&err)) != DL_OK) return st;
+  dl::CompactArgs a{};
+  a.s = s; a.hole_idx = hole_idx; a.fill_idx = fill_idx; a.move_cnt = move_cnt;
+  a.max_move = max_move; a.n_mass = n_mass; a.page_table = page_table; a.Kp = K_pool;
+  a.Vp = V_pool; a.tok_pos = tok_pos; a.tok_mass = tok_mass; a.err = err;
+  return launched(dl::launch_cache_compact(a, as_stream(stream)), "dl_cache_compact launch");
 }
 
 }  // extern "C"

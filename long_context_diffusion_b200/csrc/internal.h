@@ -119,6 +119,84 @@ cudaError_t launch_token_select(const Shape& s, const void* Q, const void* Kp,
                                 const int32_t* Kexp, int32_t* tok_pos, int32_t* tok_cnt,
                                 unsigned* err, cudaStream_t st);
 
+// Per-head norm, rotation, head split and cache append (dl_qk_norm_rope).
+struct RopeArgs {
+  Shape s;
+  const void* qkv;
+  int64_t qkv_stride;  // elements between tokens
+  int n_tok;
+  const int32_t* pos;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  const float* inv_freq;
+  int rot_dim, interleaved;
+  void* Q_out;
+  void* K_out;
+  void* V_out;
+  const int32_t* start;  // NULL: no cache append
+  const int32_t* page_table;
+  void* K_pool;
+  void* V_pool;
+  int32_t* end;
+  int32_t* tok_pos;
+  float* tok_mass;
+  int n_mass;
+  unsigned* err;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st);
+
+// Attention of one token per sequence (dl_decode_attn).
+struct DecodeArgs {
+  Shape s;
+  const void* Q;
+  const void* Kp;
+  const void* Vp;
+  const int32_t* page_table;
+  const int32_t* ctx_len;
+  void* O;
+  float* lse;       // may be NULL
+  float* tok_mass;  // may be NULL
+  int n_mass;
+  float decay;
+  void* ws;
+  unsigned* err;
+};
+size_t decode_workspace(const Shape& s);
+cudaError_t launch_decode_attn(const DecodeArgs& a, cudaStream_t st);
+
+// Eviction plan and its moves (dl_evict_select, dl_cache_compact).
+struct EvictArgs {
+  Shape s;
+  const float* tok_mass;
+  const int32_t* tok_pos;  // may be NULL
+  int n_mass;
+  const int32_t* ctx_len;
+  int budget, n_first, n_recent;
+  int32_t* hole_idx;
+  int32_t* fill_idx;
+  int max_move;
+  int32_t* move_cnt;
+  int32_t* new_len;
+  unsigned* err;
+};
+cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);
+
+struct CompactArgs {
+  Shape s;
+  const int32_t* hole_idx;
+  const int32_t* fill_idx;
+  const int32_t* move_cnt;
+  int max_move, n_mass;
+  const int32_t* page_table;
+  void* Kp;
+  void* Vp;
+  int32_t* tok_pos;  // may be NULL
+  float* tok_mass;   // may be NULL
+  unsigned* err;
+};
+cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st);
+
 // Shared by entry points in several files (defined in api.cu).
 dl_status api_check_desc(const dl_attn_desc* d, Shape* s);
 dl_status api_error_word(unsigned** out);

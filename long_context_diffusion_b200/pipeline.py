@@ -265,3 +265,94 @@ class DenoiseStep:
         e = torch.cuda.Event(enable_timing=True, external=True)
         e.record(stream)
         events.append((layer, start, e))
+
+
+def eviction_buffers(desc: A.dl_attn_desc, n_mass: int, budget: int, device):
+    """(hole_idx, fill_idx, move_cnt) of dl_evict_select for this budget."""
+    most = min(budget, max(desc.L_ctx - budget, 0))
+    return (_empty((desc.batch, n_mass, most), torch.int32, device),
+            _empty((desc.batch, n_mass, most), torch.int32, device),
+            _empty((desc.batch, n_mass), torch.int32, device))
+
+
+def evict(desc: A.dl_attn_desc, k_pool, v_pool, page_table, ctx_len, new_len, tok_mass, *,
+          budget: int, n_first: int, n_recent: int, plan, tok_pos=None, stream=None):
+    """Cuts one layer's cache to `budget` tokens per sequence: the plan
+    (dl_evict_select), then its moves (dl_cache_compact).  tok_mass
+    [batch][n_mass][L_ctx] is the attention weight its tokens have drawn: the
+    masses that dl_decode_attn keeps, or dl_sink_mass' column masses as
+    [batch][1][L_ctx].  plan = eviction_buffers(...).  The lengths after the
+    cut are written to new_len; pooled keys are the caller's to refresh."""
+    hole, fill, cnt = plan
+    A.dl_evict_select(desc, tok_mass, tok_pos, ctx_len, budget, n_first, n_recent, hole, fill, cnt,
+                      new_len, stream)
+    A.dl_cache_compact(desc, hole, fill, cnt, page_table, k_pool, v_pool, tok_pos, tok_mass,
+                       stream)
+
+
+class TokenStep:
+    """Token-by-token decoding of n_layers layers over paged caches that share
+    a page table, each sequence with its own length, optionally kept within a
+    budget of cached tokens per sequence.
+
+    A step: for every layer `attend` (norm, rotation and cache append of the
+    new token, then its attention); then once `advance`, or `evict`, which also
+    cuts every cache to the budget.  A prompt enters with `append`, followed by
+    `advance`.  Buffers are allocated once, so a step can be captured in a CUDA
+    graph.  `start` holds the cached lengths between steps.
+
+    desc: L_q 1, L_ctx the cache's capacity.  budget 0: no masses are kept."""
+
+    def __init__(self, desc: A.dl_attn_desc, n_layers: int, dtype: torch.dtype, device, *,
+                 inv_freq=None, interleaved: bool = False, eps: float = 1e-6, budget: int = 0,
+                 n_first: int = 0, n_recent: int = 0, per_head: bool = True, decay: float = 1.0):
+        self.desc, self.n_layers, self.inv_freq = desc, n_layers, inv_freq
+        self.interleaved, self.eps, self.budget = interleaved, eps, budget
+        self.n_first, self.n_recent, self.decay = n_first, n_recent, decay
+        B, H, H_kv, d, L = desc.batch, desc.H, desc.H_kv, desc.d, desc.L_ctx
+        n_mass = H_kv if per_head else 1
+        self.ws = workspace(desc, device)
+        self.start = torch.zeros((B,), dtype=torch.int32, device=device)
+        self.end = torch.zeros((B,), dtype=torch.int32, device=device)
+        self.Q = _empty((B, H, 1, d), dtype, device)
+        self.O = [_empty((B, H, d), dtype, device) for _ in range(n_layers)]
+        self.lse = [_empty((B, H), torch.float32, device) for _ in range(n_layers)]
+        self.tok_pos = self.tok_mass = [None] * n_layers
+        if budget:
+            self.tok_pos = [torch.zeros((B, n_mass, L), dtype=torch.int32, device=device)
+                            for _ in range(n_layers)]
+            self.tok_mass = [torch.zeros((B, n_mass, L), dtype=torch.float32, device=device)
+                             for _ in range(n_layers)]
+            self.plan = eviction_buffers(desc, n_mass, budget, device)
+
+    def append(self, layer: int, qkv, pos, q_weight, k_weight, k_pool, v_pool, page_table, q_out,
+               stream=None):
+        """Norm, rotation and cache append of qkv's tokens (a prompt, or the
+        step's token); their queries go to q_out [batch][H][n_tok][d]."""
+        A.dl_qk_norm_rope(self.desc, qkv, pos, q_weight, k_weight, self.eps, self.inv_freq, q_out,
+                          start=self.start, page_table=page_table, K_pool=k_pool, V_pool=v_pool,
+                          end=self.end, tok_pos=self.tok_pos[layer], tok_mass=self.tok_mass[layer],
+                          interleaved=self.interleaved, stream=stream)
+
+    def attend(self, layer: int, qkv, pos, q_weight, k_weight, k_pool, v_pool, page_table,
+               stream=None):
+        """The layer's attention output [batch][H][d] of the step's token."""
+        self.append(layer, qkv, pos, q_weight, k_weight, k_pool, v_pool, page_table, self.Q, stream)
+        A.dl_decode_attn(self.desc, self.Q, k_pool, v_pool, page_table, self.end, self.O[layer],
+                         self.lse[layer], self.ws, tok_mass=self.tok_mass[layer], decay=self.decay,
+                         stream=stream)
+        return self.O[layer]
+
+    def advance(self, stream=None):
+        """Ends a step: the appended tokens count from here on."""
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            self.start.copy_(self.end)
+
+    def evict(self, k_pools: List, v_pools: List, page_table, stream=None):
+        """Ends a step and cuts every layer's cache to the budget."""
+        for l in range(self.n_layers):
+            evict(self.desc, k_pools[l], v_pools[l], page_table, self.end, self.start,
+                  self.tok_mass[l], budget=self.budget, n_first=self.n_first,
+                  n_recent=self.n_recent, plan=self.plan, tok_pos=self.tok_pos[l], stream=stream)

@@ -57,6 +57,9 @@ from .steps import (  # noqa: F401
     gather_context, chunk_pooled_keys, chunk_scores, token_select,
     chunk_attention, dense_attention, topk_lower_index, cache_write,
 )
+from .token import (  # noqa: F401
+    norm_rotate, decode_attention, evict_plan, compact_rows, cached_rows,
+)
 from .step import (  # noqa: F401
     layer_step, chunked_step, denoise_block, StepResult, ChunkResult,
 )
