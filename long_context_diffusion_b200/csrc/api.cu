@@ -166,7 +166,7 @@ dl_status dl_workspace_size(const dl_attn_desc* desc, size_t* bytes) {
   x = dl::sinks_workspace(s);
   need = x > need ? x : need;
   if (s.L_q == 1) {  // the only descriptors dl_decode_attn takes
-    x = dl::decode_workspace(s);
+    x = dl::decode_workspace(s, true);
     need = x > need ? x : need;
   }
   *bytes = need;
@@ -499,9 +499,12 @@ dl_status dl_decode_attn(const dl_attn_desc* desc, const void* Q, const void* K_
     return fail(DL_ERR_INVALID_ARG, "dl_decode_attn: Q/K/V/O pointers must be 16-byte aligned");
   if (tok_mass && !mass_rows_ok(s, n_mass))
     return fail(DL_ERR_INVALID_ARG, "n_mass=%d (need 1 or H_kv=%d)", n_mass, s.H_kv);
+  if ((long long)s.n_slots * s.H_kv * s.page >= (1ll << 31))
+    return fail(DL_ERR_UNSUPPORTED, "dl_decode_attn: pool of %lld rows (need < 2^31)",
+                (long long)s.n_slots * s.H_kv * s.page);
   if (tok_mass && !(decay >= 0.0f && decay <= 1.0f))
     return fail(DL_ERR_INVALID_ARG, "decay=%g (need 0..1)", (double)decay);
-  if ((st = need_ws(ws, ws_bytes, dl::decode_workspace(s))) != DL_OK) return st;
+  if ((st = need_ws(ws, ws_bytes, dl::decode_workspace(s, tok_mass != nullptr))) != DL_OK) return st;
   unsigned* err = nullptr;
   if ((st = error_word(&err)) != DL_OK) return st;
   dl::DecodeArgs a{};

@@ -3,149 +3,909 @@
 //   a_t = scale q.k_t,  lse = ln sum_t e^{a_t},  o = sum_t e^{a_t - lse} v_t
 //   mass_t <- decay mass_t + sum_h e^{a_t - lse_h}
 //
-// One CTA per (sequence, query head); its warps take the keys in turn, a lane
-// holding D/32 columns, with the running maximum and sum of an online softmax
-// per warp; the warps' states are joined in shared memory.  Logits go to the
-// workspace when masses are kept, and a second kernel adds the weights.
+// Bound: HBM.  Every key and value row is read once; a KV group of G query
+// heads does 4 G d flops per 4 d bytes (bf16).
+//
+// Work split.  An item is (sequence, KV head, block of RB query heads); its
+// keys are tiles of KT.  The tiles of all items, in order, are cut into one
+// equal run per CTA, whatever the lengths are: the lengths are read on the
+// device, so a batch of very different sequences stays balanced and a single
+// long one spreads over the whole GPU.  A run is walked item by item
+// (segments).  An item inside one run is finished there; otherwise each of
+// its runs leaves a partial (maximum, sum, unnormalised output) in the
+// workspace, and the join kernel adds them in run order.
+//
+// Roles.  Warp 4 copies pages into a ring of shared-memory stages by TMA
+// (128-byte swizzle) through the page table, running ahead across segments.
+// Warps 0-3 take a quarter of each tile's keys each, with a running maximum
+// and sum of their own, so that nothing but the ring synchronises them until
+// the segment ends; then their states are added in warp order.
+//
+// bf16: S = Q K^T and O += P V on m16n8k16 tensor core instructions, fp32
+// accumulation, query heads on the M side.  Weights are fed as bf16 high and
+// low parts, p = hi + lo + O(2^-17 p), so O keeps the precision of fp32
+// weights; with at most 8 heads the two parts share one instruction (rows 0-7
+// high, 8-15 low), with 9-16 they take two.  The instruction is used because
+// a tile has at most 16 useful rows and the operands' conversion and traffic,
+// not the products, are what fills an SM here.
+// fp32: the same walk on the CUDA cores (exact products, fp32 sums): lane =
+// (key, quarter of d) for S, lane = four columns for O.
+//
+// Masses.  The main kernel leaves the logits (base-2 units) in the workspace;
+// the join kernel's other CTAs turn them into weights with the joined sums and
+// add them over the heads, in head order.
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "sm100.cuh"
+#include "tc_common.cuh"
 
 namespace dl {
 
+using namespace sm100;
+
 namespace {
 
-constexpr int kDecWarps = 8;
+constexpr int kWarps = 4;                       // computing warps
+constexpr int kThreads = (kWarps + 1) * 32;     // + the copying warp
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxCtas = 148 * kCtasPerSm;      // partial slots are sized for this many
+constexpr int kMassChunk = 1024;                // tokens of one mass CTA
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Query heads per item block: 8, or 16 for bf16 groups of more than 8.
+__host__ __device__ inline int rows_per_block(const Shape& s) {
+  return s.dtype == DL_BF16 && s.G > 8 ? 16 : 8;
+}
+__host__ __device__ inline int items_per_seq(const Shape& s) {
+  const int rb = rows_per_block(s);
+  return s.H_kv * ((s.G + rb - 1) / rb);
+}
 
 struct DecodeWs {
-  float* logit;  // [batch][H][Lp], natural units
-  float* lse;    // [batch][H]
+  long long* first;  // [batch + 1]: tiles before each sequence, then all
+  float* po;         // [2 kMaxCtas][RB][d] unnormalised partial outputs
+  float2* pml;       // [2 kMaxCtas][RB] (maximum, sum), base-2 units
+  float* lse2;       // [batch][H] of the items finished in one run, base-2
+  float* logit;      // [batch][H][Lp] base-2 (with masses)
+  int Lp;
 };
-int padded_ctx(const Shape& s) { return (s.L_ctx + 63) / 64 * 64; }
 
-DecodeWs decode_ws(void* ws, const Shape& s) {
-  DecodeWs w;
-  w.logit = reinterpret_cast<float*>(ws);
-  w.lse = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) +
-                                   round256((size_t)s.batch * s.H * padded_ctx(s) * sizeof(float)));
-  return w;
+size_t carve(const Shape& s, bool mass, void* ws, DecodeWs* w) {
+  const int rb = rows_per_block(s);
+  char* p = reinterpret_cast<char*>(ws);
+  size_t at = 0;
+  auto take = [&](size_t n) { char* q = p + at; at += round256(n); return q; };
+  DecodeWs d;
+  d.Lp = (s.L_ctx + 63) / 64 * 64;
+  d.first = reinterpret_cast<long long*>(take((size_t)(s.batch + 1) * 8));
+  d.po = reinterpret_cast<float*>(take((size_t)2 * kMaxCtas * rb * s.d * 4));
+  d.pml = reinterpret_cast<float2*>(take((size_t)2 * kMaxCtas * rb * 8));
+  d.lse2 = reinterpret_cast<float*>(take((size_t)s.batch * s.H * 4));
+  d.logit = reinterpret_cast<float*>(take(mass ? (size_t)s.batch * s.H * d.Lp * 4 : 0));
+  if (w) *w = d;
+  return at;
 }
 
-__device__ __forceinline__ int seq_len(const DecodeArgs& a, int b, bool report) {
+// Cached tokens of sequence b; a length out of range counts as 0.
+__device__ __forceinline__ int seq_len(const DecodeArgs& a, int b) {
   const int n = a.ctx_len[b];
-  if (n >= 0 && n <= a.s.L_ctx) return n;
-  if (report) flag_error(a.err, ERR_BAD_INDEX);
-  return 0;
+  return n >= 0 && n <= a.s.L_ctx ? n : 0;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kDecWarps * 32)
-decode_kernel(DecodeArgs a, float* logit, float* lse_ws, int Lp) {
-  pdl_trigger();
-  pdl_wait();
-  constexpr int C = D / 32;
-  __shared__ float s_o[kDecWarps][D], s_m[kDecWarps], s_l[kDecWarps];
-  const Shape& s = a.s;
-  const int h = blockIdx.x, b = blockIdx.y, g = h / s.G;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = seq_len(a, b, threadIdx.x == 0 && h == 0);
-  const T* q = reinterpret_cast<const T*>(a.Q) + ((size_t)b * s.H + h) * D;
-  float qv[C], o[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    qv[c] = to_f32(q[lane + 32 * c]) * (float)s.scale;
-    o[c] = 0.0f;
+// CTA that owns tile u when T tiles are cut into P runs [c T / P, (c + 1) T / P).
+__device__ __forceinline__ int run_of(long long u, long long T, int P) {
+  return (int)(((u + 1) * P - 1) / T);
+}
+
+// One run's part of an item.
+struct Segment {
+  int b, item, t0, t1, nt, len;
+};
+
+// Walks the segments of a run; every role of a CTA walks the same ones.
+struct Walk {
+  const DecodeArgs& a;
+  long long left;  // tiles of the run still to walk
+  int ips, kt, b, item, t, nt, len;
+  __device__ Walk(const DecodeArgs& a_, int ips_, int kt_, int b_, long long off, long long n)
+      : a(a_), left(n), ips(ips_), kt(kt_), b(b_) {
+    if (left <= 0) return;
+    len = seq_len(a, b);
+    nt = (len + kt - 1) / kt;
+    item = (int)(off / nt);
+    t = (int)(off % nt);
   }
-  float m = -INFINITY, l = 0.0f;
-  for (int t = warp; t < n; t += kDecWarps) {
-    const int slot = a.page_table[(size_t)b * s.n_pages + t / 64];
-    if (slot < 0 || slot >= s.n_slots) {
-      if (lane == 0) flag_error(a.err, ERR_BAD_INDEX);
-      if (lane == 0 && logit) logit[((size_t)b * s.H + h) * Lp + t] = -INFINITY;
-      continue;
+  __device__ bool next(Segment* s) {
+    if (left <= 0) return false;
+    const int n = (int)min((long long)(nt - t), left);
+    *s = Segment{b, item, t, t + n, nt, len};
+    left -= n;
+    t = 0;
+    if (left > 0 && ++item == ips) {
+      item = 0;
+      do len = seq_len(a, ++b); while (len == 0);
+      nt = (len + kt - 1) / kt;
     }
-    const size_t row = (((size_t)slot * s.H_kv + g) * 64 + t % 64) * D;
-    const T* k = reinterpret_cast<const T*>(a.Kp) + row;
-    const T* v = reinterpret_cast<const T*>(a.Vp) + row;
-    float x = 0.0f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) x = fmaf(qv[c], to_f32(k[lane + 32 * c]), x);
-    x = warp_sum(x);
-    if (lane == 0 && logit) logit[((size_t)b * s.H + h) * Lp + t] = x;
-    const float m2 = fmaxf(m, x);
-    const float keep = m == -INFINITY ? 0.0f : expf(m - m2), p = expf(x - m2);
-    l = l * keep + p;
-#pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = o[c] * keep + p * to_f32(v[lane + 32 * c]);
-    m = m2;
+    return true;
   }
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two fp32 values as bf16 high parts and bf16 remainders.
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  const float2 f = __bfloat1622float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_bf16x2(x - f.x, y - f.y);
+}
+
+template <typename T, int D_, int RB_>
+struct Cfg {
+  static constexpr int D = D_, RB = RB_;
+  static constexpr bool BF16 = sizeof(T) == 2;
+  static constexpr int KT = BF16 ? 64 : 32;            // keys per tile
+  static constexpr int BOX = KT * 128;                 // bytes of one 128-byte-wide box
+  static constexpr int BOXES = D * (int)sizeof(T) / 128;
+  static constexpr int HALF = BOX * BOXES;             // K (or V) of a stage
+  static constexpr int STAGE = 2 * HALF;
+  static constexpr int ST = 96 * 1024 / STAGE;         // stages: 96 KB of copies in flight per CTA
+  // states of the other warps at a segment's end: all three at once, or one by one
+  static constexpr int COPIES = BF16 && RB == 8 ? 3 : 1;
+  static constexpr int O_OFF = ST * STAGE;
+  static constexpr int Q_OFF = O_OFF + COPIES * RB * D * 4;        // fp32 rows of Q
+  static constexpr int P_OFF = Q_OFF + (BF16 ? 0 : RB * D * 4);    // fp32 weights [warp][RB][8]
+  static constexpr int ML_OFF = P_OFF + (BF16 ? 0 : kWarps * RB * 8 * 4);
+  static constexpr int BAR_OFF = ML_OFF + kWarps * RB * 8;
+  static constexpr int MISC_OFF = BAR_OFF + 2 * ST * 8;            // info [ST], abort
+  static constexpr int SMEM = MISC_OFF + (ST + 4) * 4 + 1024;      // + alignment slack
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+// Running state of one warp's keys of a segment, bf16.
+template <int D, int RB>
+struct StateTc {
+  static constexpr int NR = RB / 8;  // fragment rows per thread: lane/4 (and + 8)
+  float o[D / 8][4];
+  float m[NR], l[NR];
+  uint32_t q[D / 16][2 * NR];
+  __device__ __forceinline__ void reset() {
 #pragma unroll
-  for (int c = 0; c < C; ++c) s_o[warp][lane + 32 * c] = o[c];
-  if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) { m[r] = -INFINITY; l[r] = 0.0f; }
+  }
+  __device__ __forceinline__ void load_q(const __nv_bfloat16* Q, int n_rows, int lane) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int row = lane / 4 + 8 * r;
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(Q + (size_t)row * D) + (lane & 3);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        q[k][r] = row < n_rows ? p[8 * k] : 0u;
+        q[k][NR + r] = row < n_rows ? p[8 * k + 4] : 0u;
+      }
+    }
+  }
+  // 16 keys of the stage; `valid` of the tile's 64 hold tokens.
+  __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, int warp, int lane, int valid,
+                                       float c2, float* logit, int Lp, int n_rows) {
+    float s[2][4] = {};
+    {
+      const int key = warp * 16 + (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
+      const uint32_t row = ks + key * 128;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const int c = 2 * k + hi;
+        uint32_t kf[4];
+        ldsm4(row + (c >> 3) * (64 * 128) + (((c & 7) ^ (key & 7)) << 4), kf);
+        uint32_t af[4];
+        if constexpr (NR == 1) {
+          af[0] = q[k][0]; af[1] = 0u; af[2] = q[k][1]; af[3] = 0u;
+        } else {
+          af[0] = q[k][0]; af[1] = q[k][1]; af[2] = q[k][2]; af[3] = q[k][3];
+        }
+        mma16816(s[0], af, kf[0], kf[1]);
+        mma16816(s[1], af, kf[2], kf[3]);
+      }
+    }
+    const int k0 = warp * 16 + 2 * (lane & 3);  // this thread's keys: k0, k0+1, k0+8, k0+9
+    const bool part = valid < 64;
+    bool ok[2][2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) ok[n][e] = k0 + 8 * n + e < valid;
+    float x[NR][4];
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v = s[j >> 1][2 * r + (j & 1)] * c2;
+        x[r][j] = !part || ok[j >> 1][j & 1] ? v : -INFINITY;
+      }
+    if (logit) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const int row = lane / 4 + 8 * r;
+        if (row < n_rows) {
+          float* p = logit + (size_t)row * Lp + k0;
+          *reinterpret_cast<float2*>(p) = make_float2(x[r][0], x[r][1]);
+          *reinterpret_cast<float2*>(p + 8) = make_float2(x[r][2], x[r][3]);
+        }
+      }
+    }
+    bool raise = false;
+    float top[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      float t = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+      top[r] = fmaxf(m[r], t);
+      raise |= top[r] > m[r];
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float f = top[r] == -INFINITY ? 1.0f : ex2_approx(m[r] - top[r]);
+        m[r] = top[r];
+        l[r] *= f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][2 * r] *= f; o[i][2 * r + 1] *= f;
+          if (NR == 1) { o[i][2] *= f; o[i][3] *= f; }  // the low parts' sums
+        }
+      }
+    }
+    uint32_t hi[NR][2], lo[NR][2];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float base = m[r] == -INFINITY ? 0.0f : m[r];
+      float p[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = ex2_approx(x[r][j] - base);
+      l[r] += (p[0] + p[1]) + (p[2] + p[3]);
+      split_bf16(p[0], p[1], hi[r][0], lo[r][0]);
+      split_bf16(p[2], p[3], hi[r][1], lo[r][1]);
+    }
+    // rows behind the last token hold anything: their values are cleared
+    const uint32_t keep0 = (ok[0][0] ? 0xFFFFu : 0u) | (ok[0][1] ? 0xFFFF0000u : 0u);
+    const uint32_t keep1 = (ok[1][0] ? 0xFFFFu : 0u) | (ok[1][1] ? 0xFFFF0000u : 0u);
+    const int key = warp * 16 + (lane & 7) + (((lane >> 3) & 1) << 3);
+    const uint32_t row = vs + key * 128;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const int c = 2 * i + (lane >> 4);
+      uint32_t vf[4];
+      ldsm4_t(row + (c >> 3) * (64 * 128) + (((c & 7) ^ (key & 7)) << 4), vf);
+      if (part) { vf[0] &= keep0; vf[1] &= keep1; vf[2] &= keep0; vf[3] &= keep1; }
+      if constexpr (NR == 1) {
+        const uint32_t af[4] = {hi[0][0], lo[0][0], hi[0][1], lo[0][1]};
+        mma16816(o[2 * i], af, vf[0], vf[1]);
+        mma16816(o[2 * i + 1], af, vf[2], vf[3]);
+      } else {
+        const uint32_t ah[4] = {hi[0][0], hi[1][0], hi[0][1], hi[1][1]};
+        const uint32_t al[4] = {lo[0][0], lo[1][0], lo[0][1], lo[1][1]};
+        mma16816(o[2 * i], ah, vf[0], vf[1]);
+        mma16816(o[2 * i + 1], ah, vf[2], vf[3]);
+        mma16816(o[2 * i], al, vf[0], vf[1]);
+        mma16816(o[2 * i + 1], al, vf[2], vf[3]);
+      }
+    }
+  }
+  // ---- segment end
+  __device__ __forceinline__ void finish(int) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+    if constexpr (NR == 1) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) { o[i][0] += o[i][2]; o[i][1] += o[i][3]; }
+    }
+  }
+  __device__ __forceinline__ void put_ml(float2* ml, int lane) const {
+    if ((lane & 3) == 0) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) ml[lane / 4 + 8 * r] = make_float2(m[r], l[r]);
+    }
+  }
+  __device__ __forceinline__ void scale(const float* f, int lane) {  // f: per row, shared memory
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float w = f[lane / 4 + 8 * r];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) { o[i][2 * r] *= w; o[i][2 * r + 1] *= w; }
+    }
+  }
+  __device__ __forceinline__ void put(float* dst, int lane) const {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+        reinterpret_cast<float2*>(dst)[(i * NR + r) * 32 + lane] = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+  }
+  __device__ __forceinline__ void add(const float* src, int lane) {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float2 v = reinterpret_cast<const float2*>(src)[(i * NR + r) * 32 + lane];
+        o[i][2 * r] += v.x; o[i][2 * r + 1] += v.y;
+      }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(int lane, F f) const {  // f(row, column, two values)
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        f(lane / 4 + 8 * r, 8 * i + 2 * (lane & 3), make_float2(o[i][2 * r], o[i][2 * r + 1]));
+  }
+};
+
+// Running state of one warp's keys of a segment, fp32: o holds columns
+// 4 (lane % (D/4)) .. + 3, of every second key when D is 64.
+template <int D, int RB>
+struct StateF32 {
+  static constexpr int CH = D / 4;          // 16-byte columns of a row
+  static constexpr int KS = 32 / CH;        // keys taken at a time by the P V lanes
+  float o[RB][4];
+  float m[RB], l[RB];                       // l: of this lane's key
+  const float* sq;                          // Q rows in shared memory [RB][D]
+  float* sp;                                // this warp's weights [RB][8]
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.0f;
+      m[r] = -INFINITY; l[r] = 0.0f;
+    }
+  }
+  __device__ __forceinline__ static uint32_t chunk_at(int key, int c) {
+    return (c >> 3) * (32 * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
+  }
+  __device__ __forceinline__ void tile(const char* ks, const char* vs, int warp, int lane, int valid,
+                                       float c2, float* logit, int Lp, int n_rows) {
+    const int kk = lane & 7, key = warp * 8 + kk, dq = lane >> 3;
+    float x[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) x[r] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < CH / 4; ++j) {
+      const int c = 4 * j + dq;
+      const float4 k = *reinterpret_cast<const float4*>(ks + chunk_at(key, c));
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        const float4 q = *reinterpret_cast<const float4*>(sq + r * D + 4 * c);
+        x[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, x[r]))));
+      }
+    }
+    const bool ok = key < valid;
+    bool raise = false;
+    float top[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      x[r] += __shfl_xor_sync(0xffffffffu, x[r], 8);
+      x[r] += __shfl_xor_sync(0xffffffffu, x[r], 16);
+      x[r] = ok ? x[r] * c2 : -INFINITY;
+      if (logit && dq == 0 && r < n_rows) logit[(size_t)r * Lp + key] = x[r];
+      float t = x[r];
+#pragma unroll
+      for (int w = 1; w < 8; w <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, w));
+      top[r] = fmaxf(m[r], t);
+      raise |= top[r] > m[r];
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        const float f = top[r] == -INFINITY ? 1.0f : ex2_approx(m[r] - top[r]);
+        m[r] = top[r];
+        l[r] *= f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[r][e] *= f;
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const float p = ex2_approx(x[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
+      l[r] += p;
+      if (dq == (r & 3)) sp[r * 8 + kk] = p;
+    }
+    __syncwarp();
+    const int c = lane % CH, ks0 = lane / CH;
+#pragma unroll
+    for (int k = 0; k < 8; k += KS) {
+      const int kl = k + ks0;
+      float4 v = *reinterpret_cast<const float4*>(vs + chunk_at(warp * 8 + kl, c));
+      if (warp * 8 + kl >= valid) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // behind the last token
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        const float p = sp[r * 8 + kl];
+        o[r][0] = fmaf(p, v.x, o[r][0]);
+        o[r][1] = fmaf(p, v.y, o[r][1]);
+        o[r][2] = fmaf(p, v.z, o[r][2]);
+        o[r][3] = fmaf(p, v.w, o[r][3]);
+      }
+    }
+  }
+  __device__ __forceinline__ void finish(int) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+#pragma unroll
+      for (int w = 1; w < 8; w <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
+      if constexpr (KS == 2) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[r][e] += __shfl_xor_sync(0xffffffffu, o[r][e], 16);
+      }
+    }
+  }
+  __device__ __forceinline__ void put_ml(float2* ml, int lane) const {
+    if (lane == 0) {
+#pragma unroll
+      for (int r = 0; r < RB; ++r) ml[r] = make_float2(m[r], l[r]);
+    }
+  }
+  __device__ __forceinline__ void scale(const float* f, int) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const float w = f[r];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[r][e] *= w;
+    }
+  }
+  __device__ __forceinline__ void put(float* dst, int lane) const {
+    if (lane >= CH) return;
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+      reinterpret_cast<float4*>(dst)[r * CH + lane] = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+  }
+  __device__ __forceinline__ void add(const float* src, int lane) {
+    if (lane >= CH) return;
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const float4 v = reinterpret_cast<const float4*>(src)[r * CH + lane];
+      o[r][0] += v.x; o[r][1] += v.y; o[r][2] += v.z; o[r][3] += v.w;
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(int lane, F f) const {
+    if (lane >= CH) return;
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      f(r, 4 * lane, make_float2(o[r][0], o[r][1]));
+      f(r, 4 * lane + 2, make_float2(o[r][2], o[r][3]));
+    }
+  }
+};
+
+__device__ __forceinline__ void store2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.x, v.y);
+}
+
+template <typename T, int D, int RB>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+              const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodeWs ws) {
+  using C = Cfg<T, D, RB>;
+  extern __shared__ char smem_raw[];
+  char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
+  uint64_t* empty = full + C::ST;
+  volatile int* info = reinterpret_cast<volatile int*>(sm + C::MISC_OFF);
+  volatile int* abort_flag = info + C::ST;
+  __shared__ long long s_scan[kThreads / 32], s_off;
+  __shared__ int s_b;
+  __shared__ float s_f[kWarps][RB];
+  const Shape& s = a.s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nrb = (s.G + RB - 1) / RB, ips = s.H_kv * nrb;
+  if (tid == 0) {
+    for (int i = 0; i < C::ST; ++i) { mbar_init(full + i, 1); mbar_init(empty + i, kWarps); }
+    fence_mbar_init();
+    *abort_flag = 0;
+  }
+  if (warp == kWarps && lane == 0) { prefetch_tmap(&mk); prefetch_tmap(&mv); }
+  pdl_wait();
+
+  // This CTA's run: tiles [lo, hi) of the total of all sequences.  Each thread
+  // counts a run of sequences; the one whose count reaches lo finds the place.
+  const int per = (s.batch + kThreads - 1) / kThreads, b0 = min(s.batch, tid * per),
+            b1 = min(s.batch, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = a.ctx_len[b];
+    if (n < 0 || n > s.L_ctx) {
+      if (blockIdx.x == 0) flag_error(a.err, ERR_BAD_INDEX);
+    } else {
+      mine += (long long)((n + C::KT - 1) / C::KT) * ips;
+    }
+  }
+  long long before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  if (lane == 31) s_scan[warp] = before;
+  before -= mine;
   __syncthreads();
-  if (threadIdx.x < D) {
-    float M = -INFINITY, L = 0.0f, acc = 0.0f;
-    for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, s_m[w]);
-    for (int w = 0; w < kDecWarps; ++w) {
-      if (s_m[w] == -INFINITY) continue;
-      const float f = expf(s_m[w] - M);
-      L += s_l[w] * f;
-      acc += s_o[w][threadIdx.x] * f;
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  const int P = (int)min((long long)gridDim.x, total);  // runs that hold a tile
+  const int c = blockIdx.x;
+  if (c == 0) {  // for the join kernel
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      ws.first[b] = at;
+      at += (long long)((seq_len(a, b) + C::KT - 1) / C::KT) * ips;
     }
-    reinterpret_cast<T*>(a.O)[((size_t)b * s.H + h) * D + threadIdx.x] =
-        from_f32<T>(L > 0.0f ? acc / L : 0.0f);
-    if (threadIdx.x == 0) {
-      const float lse = L > 0.0f ? M + logf(L) : -INFINITY;
-      if (a.lse) a.lse[(size_t)b * s.H + h] = lse;
-      lse_ws[(size_t)b * s.H + h] = lse;
+    if (tid == 0) ws.first[s.batch] = total;
+  }
+  if (c >= P) return;
+  const long long lo = total * c / P, hi = total * (c + 1) / P;
+  if (lo >= before && lo < before + mine) {
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const long long w = (long long)((seq_len(a, b) + C::KT - 1) / C::KT) * ips;
+      if (lo < at + w) { s_b = b; s_off = lo - at; break; }
+      at += w;
+    }
+  }
+  __syncthreads();
+  Walk walk(a, ips, C::KT, s_b, s_off, hi - lo);
+  Segment seg;
+
+  if (warp == kWarps) {
+    // ---- copies
+    int k = 0, have_b = -1, have_t = 0, slots = 0;
+    bool dead = false;
+    while (walk.next(&seg)) {
+      const int g = seg.item / nrb;
+      for (int base = seg.t0; base < seg.t1; base += 32) {
+        // 32 tiles' pages at a time; the next KV head of a short sequence reuses them
+        if (seg.b != have_b || base < have_t || min(base + 32, seg.t1) > have_t + 32) {
+          const int t = base + lane;
+          slots = t < seg.nt ? a.page_table[(size_t)seg.b * s.n_pages + (t * C::KT) / 64] : -1;
+          have_b = seg.b;
+          have_t = base;
+        }
+        const int n = min(32, seg.t1 - base);
+        for (int j = 0; j < n; ++j, ++k) {
+          const int slot = __shfl_sync(0xffffffffu, slots, base - have_t + j);
+          if (lane != 0) continue;
+          const int st = k % C::ST;
+          if (!dead && k >= C::ST) dead = !mbar_wait(empty + st, (k / C::ST - 1) & 1, abort_flag);
+          if (dead) continue;
+          const int tile = base + j;
+          if (slot < 0 || slot >= s.n_slots) {
+            flag_error(a.err, ERR_BAD_INDEX);
+            info[st] = 0;
+            mbar_arrive(full + st);
+            continue;
+          }
+          info[st] = min(C::KT, seg.len - tile * C::KT);
+          mbar_arrive_expect_tx(full + st, C::STAGE);
+          const int y = (slot * s.H_kv + g) * 64 + (tile * C::KT) % 64;
+          char* dst = sm + st * C::STAGE;
+#pragma unroll
+          for (int x = 0; x < C::BOXES; ++x) {
+            tma_load_2d(dst + x * C::BOX, &mk, x * (128 / (int)sizeof(T)), y, full + st);
+            tma_load_2d(dst + C::HALF + x * C::BOX, &mv, x * (128 / (int)sizeof(T)), y, full + st);
+          }
+        }
+      }
+    }
+    if (lane == 0 && *abort_flag) {  // gave up: wait (bounded) for the copies in flight
+      flag_error(a.err, ERR_TIMEOUT);
+      for (int i = max(0, k - C::ST); i < k; ++i)
+        for (uint32_t n = 0; n < 4096 && !mbar_try_wait(full + i % C::ST, (i / C::ST) & 1); ++n) {}
+    }
+    return;
+  }
+
+  // ---- computing warps
+  using State = typename std::conditional<C::BF16, StateTc<D, RB>, StateF32<D, RB>>::type;
+  State st8;
+  float* s_o = reinterpret_cast<float*>(sm + C::O_OFF);
+  float2* s_ml = reinterpret_cast<float2*>(sm + C::ML_OFF);
+  const float c2 = (float)(s.scale * 1.4426950408889634);
+  int k = 0;
+  bool dead = false;
+  while (walk.next(&seg)) {
+    const int g = seg.item / nrb, r0 = (seg.item % nrb) * RB, n_rows = min(RB, s.G - r0);
+    const size_t row0 = (size_t)seg.b * s.H + g * s.G + r0;  // the block's first (b, h)
+    const T* q = reinterpret_cast<const T*>(a.Q) + row0 * D;
+    if constexpr (C::BF16) {
+      st8.load_q(q, n_rows, lane);
+    } else {
+      float* sq = reinterpret_cast<float*>(sm + C::Q_OFF);
+      named_bar_sync(1, kWarps * 32);  // the last segment's rows are no longer read
+      for (int e = tid; e < RB * D; e += kWarps * 32) sq[e] = e < n_rows * D ? q[e] : 0.0f;
+      named_bar_sync(1, kWarps * 32);
+      st8.sq = sq;
+      st8.sp = reinterpret_cast<float*>(sm + C::P_OFF) + warp * RB * 8;
+    }
+    st8.reset();
+    for (int t = seg.t0; t < seg.t1; ++t, ++k) {
+      const int st = k % C::ST;
+      if (!dead) dead = !mbar_wait(full + st, (k / C::ST) & 1, abort_flag);
+      if (__any_sync(0xffffffffu, dead)) { dead = true; continue; }
+      const int valid = info[st];
+      float* logit = a.tok_mass ? ws.logit + row0 * ws.Lp + (size_t)t * C::KT : nullptr;
+      if constexpr (C::BF16) {
+        const uint32_t ks = smem_u32(sm + st * C::STAGE);
+        st8.tile(ks, ks + C::HALF, warp, lane, valid, c2, logit, ws.Lp, n_rows);
+      } else {
+        const char* ks = sm + st * C::STAGE;
+        st8.tile(ks, ks + C::HALF, warp, lane, valid, c2, logit, ws.Lp, n_rows);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + st);
+    }
+    // segment end: the four warps' states, added in warp order
+    st8.finish(lane);
+    st8.put_ml(s_ml + warp * RB, lane);
+    named_bar_sync(1, kWarps * 32);
+    if (lane < RB) {
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * RB + lane].x);
+      const float own = s_ml[warp * RB + lane].x;
+      s_f[warp][lane] = own == -INFINITY ? 0.0f : ex2_approx(own - M);
+    }
+    __syncwarp();
+    st8.scale(s_f[warp], lane);
+    float M = -INFINITY, L = 0.0f;  // row `lane`, on warp 0
+    if (warp == 0 && lane < RB) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * RB + lane].x);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 v = s_ml[w * RB + lane];
+        if (v.x != -INFINITY) L = fmaf(v.y, ex2_approx(v.x - M), L);
+      }
+    }
+#pragma unroll
+    for (int w0 = 1; w0 < kWarps; w0 += C::COPIES) {
+      if (warp >= w0 && warp < w0 + C::COPIES) st8.put(s_o + (warp - w0) * RB * D, lane);
+      named_bar_sync(1, kWarps * 32);
+      if (warp == 0) {
+#pragma unroll
+        for (int w = 0; w < C::COPIES; ++w) st8.add(s_o + w * RB * D, lane);
+      }
+      if (w0 + C::COPIES < kWarps) named_bar_sync(1, kWarps * 32);
+    }
+    if (warp != 0) continue;
+    if (seg.t0 == 0 && seg.t1 == seg.nt) {
+      float inv = L > 0.0f ? 1.0f / L : 0.0f;
+      if (L != L) inv = L;
+      if (lane < n_rows) {
+        const float lse2 = L > 0.0f ? M + log2f(L) : (L != L ? L : -INFINITY);
+        ws.lse2[row0 + lane] = lse2;
+        if (a.lse) a.lse[row0 + lane] = lse2 * kLn2;
+      }
+      T* O = reinterpret_cast<T*>(a.O) + row0 * D;
+      __syncwarp();
+      if (lane < RB) s_f[0][lane] = inv;
+      __syncwarp();
+      st8.each(lane, [&](int r, int col, float2 v) {
+        const float f = s_f[0][r];
+        if (r < n_rows) store2(O + (size_t)r * D + col, make_float2(v.x * f, v.y * f));
+      });
+    } else {
+      const int slot = 2 * c + (seg.t0 == 0 ? 1 : 0);
+      if (lane < n_rows) ws.pml[(size_t)slot * RB + lane] = make_float2(M, L);
+      float* po = ws.po + (size_t)slot * RB * D;
+      st8.each(lane, [&](int r, int col, float2 v) {
+        if (r < n_rows) store2(po + (size_t)r * D + col, v);
+      });
     }
   }
 }
 
-__global__ void decode_mass_kernel(DecodeArgs a, const float* logit, const float* lse_ws, int Lp) {
-  pdl_trigger();
+// The partials of one item: runs c0..c1 and their slots.
+struct Parts {
+  int c0, n, r;  // first run, number of runs, row in the block
+  __device__ __forceinline__ int slot(int i) const { return 2 * (c0 + i) + (i == 0 ? 1 : 0); }
+};
+__device__ __forceinline__ Parts parts_of(const DecodeArgs& a, const DecodeWs& ws, int P0, int b, int h,
+                                          int rb, int kt) {
+  const Shape& s = a.s;
+  const int g = h / s.G, nrb = (s.G + rb - 1) / rb, r = h % s.G;
+  const long long T = ws.first[s.batch];
+  const int P = (int)min((long long)P0, T), nt = (seq_len(a, b) + kt - 1) / kt;
+  Parts p;
+  p.r = r % rb;
+  if (nt == 0) { p.c0 = p.n = 0; return p; }
+  const long long u0 = ws.first[b] + (long long)(g * nrb + r / rb) * nt;
+  p.c0 = run_of(u0, T, P);
+  p.n = run_of(u0 + nt - 1, T, P) - p.c0 + 1;
+  return p;
+}
+
+// CTAs [0, batch * H): join the partials of one query row (or write an empty
+// sequence's row).  The others: masses of kMassChunk tokens at a time.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodeWs ws, int P0,
+                   int rb, int kt, int chunks) {
   pdl_wait();
   const Shape& s = a.s;
-  const int b = blockIdx.y / a.n_mass, m = blockIdx.y % a.n_mass;
-  const int n = seq_len(a, b, false), rows = s.H / a.n_mass;
-  for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < n; t += gridDim.x * blockDim.x) {
-    float sum = 0.0f;
-    for (int r = 0; r < rows; ++r) {
-      const size_t row = (size_t)b * s.H + m * rows + r;
-      const float lse = lse_ws[row];
-      if (lse != -INFINITY) sum += expf(logit[row * Lp + t] - lse);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (blockIdx.x < s.batch * s.H) {
+    __shared__ float s_m[8], s_l[8];
+    __shared__ float4 s_o[256];
+    const int row = blockIdx.x, b = row / s.H;
+    const Parts p = parts_of(a, ws, P0, b, row % s.H, rb, kt);
+    if (p.n == 1) return;  // finished by its run
+    // maximum and sum over the runs
+    float M = -INFINITY, L = 0.0f;
+    for (int i = tid; i < p.n; i += 256) M = fmaxf(M, ws.pml[(size_t)p.slot(i) * rb + p.r].x);
+    M = warp_max(M);
+    if (lane == 0) s_m[warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) M = fmaxf(M, s_m[w]);
+    for (int i = tid; i < p.n; i += 256) {
+      const float2 v = ws.pml[(size_t)p.slot(i) * rb + p.r];
+      if (v.x != -INFINITY) L = fmaf(v.y, ex2_approx(v.x - M), L);
     }
-    float* dst = a.tok_mass + ((size_t)b * a.n_mass + m) * s.L_ctx + t;
-    *dst = a.decay == 0.0f ? sum : fmaf(a.decay, *dst, sum);
+    L = warp_sum(L);
+    if (lane == 0) s_l[warp] = L;
+    // outputs: thread = (part group, four columns)
+    constexpr int CH = D / 4, GR = 256 / CH;
+    const int col = tid % CH, grp = tid / CH;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = grp; i < p.n; i += GR) {
+      const size_t at = (size_t)p.slot(i) * rb + p.r;
+      const float m = ws.pml[at].x;
+      const float4 v = reinterpret_cast<const float4*>(ws.po)[at * CH + col];
+      const float f = m == -INFINITY ? 0.0f : ex2_approx(m - M);
+      o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y);
+      o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+    }
+    s_o[tid] = o;
+    __syncthreads();
+    L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) L += s_l[w];
+    if (tid < CH) {
+      for (int i = 1; i < GR; ++i) {
+        const float4 v = s_o[i * CH + tid];
+        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+      }
+      float inv = L > 0.0f ? 1.0f / L : 0.0f;
+      if (L != L) inv = L;
+      T* dst = reinterpret_cast<T*>(a.O) + (size_t)row * D + 4 * tid;
+      store2(dst, make_float2(o.x * inv, o.y * inv));
+      store2(dst + 2, make_float2(o.z * inv, o.w * inv));
+    }
+    if (tid == 0 && a.lse)
+      a.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : (L != L ? L : -INFINITY);
+    return;
   }
+  // ---- masses
+  __shared__ float s_lse[32];
+  const int id = blockIdx.x - s.batch * s.H;
+  const int bm = id / chunks, b = bm / a.n_mass, m = bm % a.n_mass;
+  const int n = seq_len(a, b), rows = s.H / a.n_mass, h0 = m * rows;
+  for (int t0 = (id % chunks) * kMassChunk; t0 < n; t0 += chunks * kMassChunk) {
+    float sum[kMassChunk / 256];
+#pragma unroll
+    for (int j = 0; j < kMassChunk / 256; ++j) sum[j] = 0.0f;
+    for (int r0 = 0; r0 < rows; r0 += 32) {
+      // the rows' sums, eight lanes a row
+      __syncthreads();
+      const int r = r0 + tid / 8, ln = tid % 8;
+      float M = -INFINITY, L = 0.0f, lse = INFINITY;
+      if (r < rows) {
+        const Parts p = parts_of(a, ws, P0, b, h0 + r, rb, kt);
+        if (p.n == 1) {
+          lse = ws.lse2[(size_t)b * s.H + h0 + r];
+        } else {
+          for (int i = ln; i < p.n; i += 8) M = fmaxf(M, ws.pml[(size_t)p.slot(i) * rb + p.r].x);
+#pragma unroll
+          for (int w = 1; w < 8; w <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffu << (lane & 24), M, w));
+          for (int i = ln; i < p.n; i += 8) {
+            const float2 v = ws.pml[(size_t)p.slot(i) * rb + p.r];
+            if (v.x != -INFINITY) L = fmaf(v.y, ex2_approx(v.x - M), L);
+          }
+#pragma unroll
+          for (int w = 1; w < 8; w <<= 1) L += __shfl_xor_sync(0xffu << (lane & 24), L, w);
+          lse = M + log2f(L);
+        }
+      }
+      if (ln == 0) s_lse[tid / 8] = lse == -INFINITY ? INFINITY : lse;  // no weight at all: 2^-inf
+      __syncthreads();
+      const int nr = min(32, rows - r0);
+      const float* x = ws.logit + ((size_t)b * s.H + h0 + r0) * ws.Lp + t0 + tid;
+#pragma unroll 4
+      for (int q = 0; q < nr; ++q) {
+        const float l2 = s_lse[q];
+#pragma unroll
+        for (int j = 0; j < kMassChunk / 256; ++j)
+          if (t0 + tid + 256 * j < n) sum[j] += ex2_approx(x[(size_t)q * ws.Lp + 256 * j] - l2);
+      }
+    }
+    float* dst = a.tok_mass + ((size_t)b * a.n_mass + m) * s.L_ctx + t0 + tid;
+#pragma unroll
+    for (int j = 0; j < kMassChunk / 256; ++j) {
+      if (t0 + tid + 256 * j < n)
+        dst[256 * j] = a.decay == 0.0f ? sum[j] : fmaf(a.decay, dst[256 * j], sum[j]);
+    }
+  }
+}
+
+template <typename T, int D, int RB>
+cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
+  using C = Cfg<T, D, RB>;
+  const Shape& s = a.s;
+  DecodeWs w;
+  carve(s, a.tok_mass != nullptr, a.ws, &w);
+  const uint64_t rows = (uint64_t)s.n_slots * s.H_kv * 64;
+  CUtensorMap mk, mv;
+  const bool ok = C::BF16 ? tc_map_2d(&mk, a.Kp, D, rows, C::KT) && tc_map_2d(&mv, a.Vp, D, rows, C::KT)
+                          : tc_map_f32_2d(&mk, a.Kp, D, rows, C::KT) &&
+                                tc_map_f32_2d(&mv, a.Vp, D, rows, C::KT);
+  if (!ok) return cudaErrorInvalidValue;
+  auto kern = decode_kernel<T, D, RB>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long most = (long long)s.batch * items_per_seq(s) * ((s.L_ctx + C::KT - 1) / C::KT);
+  int P = tc_sm_count() * kCtasPerSm;
+  P = P < kMaxCtas ? P : kMaxCtas;
+  P = (int)(most < P ? (most > 0 ? most : 1) : P);
+  DL_LAUNCH(kern, P, kThreads, C::SMEM, st, mk, mv, a, w);
+  int chunks = 0;
+  if (a.tok_mass && s.L_ctx > 0) {
+    chunks = (s.L_ctx + kMassChunk - 1) / kMassChunk;
+    chunks = chunks < 4096 ? chunks : 4096;
+  }
+  auto join = decode_join_kernel<T, D>;
+  DL_LAUNCH(join, s.batch * s.H + s.batch * a.n_mass * chunks, 256, 0, st, a, w, P, RB, C::KT,
+            chunks > 0 ? chunks : 1);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t decode_workspace(const Shape& s) {
-  return round256((size_t)s.batch * s.H * padded_ctx(s) * sizeof(float)) +
-         round256((size_t)s.batch * s.H * sizeof(float));
-}
+size_t decode_workspace(const Shape& s, bool mass) { return carve(s, mass, nullptr, nullptr); }
 
 cudaError_t launch_decode_attn(const DecodeArgs& a, cudaStream_t st) {
   const Shape& s = a.s;
-  const DecodeWs w = decode_ws(a.ws, s);
-  const int Lp = padded_ctx(s);
-  float* logit = a.tok_mass ? w.logit : nullptr;
-#define DL_DEC(T, D_) \
-  DL_LAUNCH((decode_kernel<T, D_>), dim3(s.H, s.batch), kDecWarps * 32, 0, st, a, logit, w.lse, Lp)
   if (s.dtype == DL_BF16) {
-    if (s.d == 128) DL_DEC(__nv_bfloat16, 128); else DL_DEC(__nv_bfloat16, 64);
-  } else {
-    if (s.d == 128) DL_DEC(float, 128); else DL_DEC(float, 64);
+    if (s.d == 128)
+      return s.G > 8 ? run_decode<__nv_bfloat16, 128, 16>(a, st) : run_decode<__nv_bfloat16, 128, 8>(a, st);
+    return s.G > 8 ? run_decode<__nv_bfloat16, 64, 16>(a, st) : run_decode<__nv_bfloat16, 64, 8>(a, st);
   }
-#undef DL_DEC
-  if (a.tok_mass && s.L_ctx > 0) {
-    const int chunks = min((s.L_ctx + 255) / 256, 64);
-    DL_LAUNCH(decode_mass_kernel, dim3(chunks, s.batch * a.n_mass), 256, 0, st, a, (const float*)logit,
-              (const float*)w.lse, Lp);
-  }
-  return cudaGetLastError();
+  return s.d == 128 ? run_decode<float, 128, 8>(a, st) : run_decode<float, 64, 8>(a, st);
 }
 
 }  // namespace dl

@@ -162,7 +162,7 @@ struct DecodeArgs {
   void* ws;
   unsigned* err;
 };
-size_t decode_workspace(const Shape& s);
+size_t decode_workspace(const Shape& s, bool mass);
 cudaError_t launch_decode_attn(const DecodeArgs& a, cudaStream_t st);
 
 // Eviction plan and its moves (dl_evict_select, dl_cache_compact).

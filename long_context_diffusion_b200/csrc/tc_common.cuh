@@ -77,6 +77,9 @@ __device__ __forceinline__ int2 tc_tile_info(const AttnArgs& a, int bg, int tile
 // ---- host side (attn_tc.cu) ----
 // bf16 rows of `inner` elements, boxes of 64 x box_rows, 128-byte swizzle.
 bool tc_map_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows);
+// fp32 rows of `inner` elements, boxes of 32 x box_rows, 128-byte swizzle.
+bool tc_map_f32_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
+                   uint32_t box_rows);
 // decode block K/V: [bg][L_q][d], boxes of 64 x 64 x 1 (rows past L_q read 0)
 bool tc_map_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t L_q, uint64_t n_bg);
 // int8 planes [planes][rows][inner] (inner = 128 bytes), boxes of
