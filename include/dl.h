@@ -376,7 +376,8 @@ dl_status dl_block_scores_noalloc(const dl_attn_desc* desc, const void* Q_dec,
  *     sequence, shared by its KV heads) or H_kv (one per KV head).
  *       tok_mass fp32  [batch][n_mass][L_ctx]  accumulated attention weight
  *       tok_pos  int32 [batch][n_mass][L_ctx]  position in the sequence
- *     Entries at or behind a sequence's length are neither read nor written.
+ *     Entries at or behind a sequence's length count for nothing and are not
+ *     written.
  *   - These calls do not keep the pooled keys of dl_pool_keys up to date:
  *     call dl_pool_keys before the next block selection over this cache.
  *   - Buffers that a call writes must not overlap any other buffer of the

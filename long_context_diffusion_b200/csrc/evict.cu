@@ -6,19 +6,21 @@
 //
 // Bound: latency (a row of n tokens is 8 n bytes; 128 rows of 32K, 38 MB, are
 // 6 us of HBM).  A decision row is taken by a cluster of 1 to 8 CTAs that
-// splits it in index order and keeps its keys in registers, so that masses and
-// positions are read once; a warp owns 32 E consecutive tokens and reads them
-// coalesced, lane l of iteration j holding token 32 j + l.
+// splits its n tokens evenly in index order and keeps their keys in shared
+// memory, so that masses and positions are read once; a warp owns 32 it
+// consecutive tokens, lane l of iteration j having token 32 j + l.
 //  - The budget-th key by radix select: a histogram of the top 12 bits (sign,
 //    exponent, three bits of mantissa), then of the next 10 and the last 10
-//    among the keys that share the digits found.  The CTAs' counts are added
-//    through the cluster's shared memory by every CTA for itself.  The search
-//    ends at the first digit whose whole bin stays.
+//    among the keys that share the digits found.  Each CTA counts its own
+//    tokens and sums its bins by groups of 32; every CTA then adds the groups'
+//    sums over the cluster, finds the group, and adds that group's 32 bins
+//    alone (adding all bins over the cluster took four times as long).  The
+//    search ends at the first digit whose whole bin stays.
 //  - One vote per iteration gives the 32 tokens' keep bits as a word, lane j
 //    holding iteration j's; holes and fills are then counted and listed by
 //    words, with prefix sums over lanes, warps and CTAs.
-// Rows too long for the registers (E = 0) recompute their keys from memory in
-// every pass.
+// Rows too long for the cluster's shared memory (KEEP false) recompute their
+// keys from memory in every pass.
 //
 // Moves: bound by HBM (each moved row is read and written once).  A warp
 // resolves 32 moves at a time, one per lane, then all lanes copy their rows in
@@ -35,7 +37,7 @@ namespace {
 constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kRegTokens = 32;           // most tokens of a thread kept in registers
+constexpr int kKeepTokens = 48;          // most tokens of a thread kept in shared memory (192 KB)
 constexpr unsigned kHeldKey = 0xFF800000u;  // the key of +infinity
 
 // Order-preserving bits of a mass: a < b as numbers <=> key(a) < key(b);
@@ -63,18 +65,6 @@ __device__ __forceinline__ int peer_int(const int* p, unsigned rank) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
   return v;
 }
-__device__ __forceinline__ int4 peer_int4(const int* p, unsigned rank) {
-  const unsigned here = static_cast<unsigned>(__cvta_generic_to_shared(p));
-  unsigned there;
-  int4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(there)
-               : "memory");
-  return v;
-}
-
 __device__ __forceinline__ int warp_inclusive(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -84,26 +74,25 @@ __device__ __forceinline__ int warp_inclusive(int v, int lane) {
   return v;
 }
 
-// E: tokens per thread in registers; 0: keys recomputed from memory, NB blocks
-// of 1024 tokens per warp.
-template <int E>
+// KEEP: keys in shared memory; else recomputed from memory.
+template <bool KEEP>
 __global__ void __launch_bounds__(kEvThreads, 1)
-evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int blocks) {
-  constexpr int ITERS = E ? E : 32;      // iterations of one block of a warp
-  __shared__ __align__(16) int s_h0[4096];
-  __shared__ int s_h1[1024], s_h2[1024];
+evict_select_kernel(const __grid_constant__ EvictArgs a, int cs) {
+  extern __shared__ unsigned s_key[];
+  __shared__ __align__(16) int s_hist[4096 + 2 * 1024];
+  __shared__ int s_group[3][128];        // this CTA's counts of 32 bins
+  __shared__ int s_gsum[128], s_bsum[32];  // the cluster's
   __shared__ int s_wt[3][kEvWarps];      // per warp: ties, holes, fills
   __shared__ int s_ct[4];                // this CTA's: largest position, ties, holes, fills
-  __shared__ int s_scan[kEvWarps], s_pick[3], s_max[kEvWarps];
+  __shared__ int s_max[kEvWarps];
   const Shape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const unsigned rank = cs > 1 ? cluster_rank() : 0u;
+  const int rank = cs > 1 ? (int)cluster_rank() : 0;
   const int row = blockIdx.x / cs, b = row / a.n_mass;
   pdl_trigger();
-  for (int i = tid; i < 4096; i += kEvThreads) s_h0[i] = 0;
-  s_h1[tid] = s_h2[tid] = 0;
   pdl_wait();
   const int n = a.ctx_len[b];
+  for (int i = tid; i < 4096 + 2 * 1024; i += kEvThreads) s_hist[i] = 0;
   const bool bad = n < 0 || n > s.L_ctx;
   if (tid == 0 && rank == 0 && row % a.n_mass == 0) {
     if (bad) flag_error(a.err, ERR_BAD_INDEX);
@@ -115,21 +104,29 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int blocks) {
   if (!bad && n > a.budget) {            // the same for the whole cluster
     const float* mass = a.tok_mass + (size_t)row * s.L_ctx;
     const int32_t* pos = a.tok_pos ? a.tok_pos + (size_t)row * s.L_ctx : nullptr;
-    // first token of this warp's block k
-    auto block_at = [&](int k) {
-      return (((long long)rank * kEvWarps + warp) * blocks + k) * (32 * ITERS);
-    };
-    unsigned key[E ? E : 1];
-    // largest position
-    int last = INT32_MIN;
-    for (int k = 0; k < blocks; ++k) {
-      const long long t0 = block_at(k) + lane;
+    // this warp's tokens [w0, w0 + 32 it) (those below n exist); 64-bit: the
+    // last warps' may lie past 2^31
+    const int it = (int)(((long long)n + cs * kEvThreads - 1) / (cs * kEvThreads));
+    const long long w0 = ((long long)rank * kEvWarps + warp) * 32 * it;
+    const int live = (int)max(0ll, min((long long)it, ((long long)n - w0 + 31) / 32));  // iterations
+    unsigned* keys = s_key + warp * 32 * it + lane;
+    // Loads are unconditional (indices clamped to the row), so that a thread's
+    // are all in flight together; the first masses do not wait for the largest
+    // position.
+    constexpr int U = 8;
+    auto index = [&](int j) { return (int)min(w0 + 32 * j + lane, (long long)n - 1); };
+    float m0[U];
 #pragma unroll
-      for (int j = 0; j < ITERS; ++j) {
-        const long long t = t0 + 32 * j;
-        const int p = t < n ? (pos ? pos[t] : (int)t) : INT32_MIN;
-        last = max(last, p);
-        if constexpr (E > 0) key[j] = (unsigned)p;
+    for (int u = 0; u < U; ++u) m0[u] = mass[index(u)];
+    int last = INT32_MIN;
+    for (int j0 = 0; j0 < live; j0 += U) {
+      int p[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) p[u] = pos ? pos[index(j0 + u)] : index(j0 + u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        last = max(last, p[u]);          // a clamped index repeats a token of the row
+        if (KEEP && j0 + u < live) keys[32 * (j0 + u)] = (unsigned)p[u];
       }
     }
     last = __reduce_max_sync(0xffffffffu, last);
@@ -139,100 +136,117 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int blocks) {
     if (cs > 1) {
       if (tid == 0) s_ct[0] = last;
       cluster_sync();
-      for (int r = 0; r < cs; ++r) last = max(last, peer_int(&s_ct[0], r));
+      last = __reduce_max_sync(0xffffffffu, lane < cs ? peer_int(&s_ct[0], lane) : INT32_MIN);
     }
     const long long recent = (long long)last - a.n_recent;
-    auto key_of = [&](long long t, int p) {
-      return (p < a.n_first || p > recent) ? kHeldKey : mass_key(mass[t]);
+    auto key_of = [&](long long t, int p, float m) {
+      return t >= n ? 0u : (p < a.n_first || p > recent) ? kHeldKey : mass_key(m);
     };
-    if constexpr (E > 0) {
-      const long long t0 = block_at(0) + lane;
+    if (KEEP) {
+#pragma unroll 1
+      for (int j0 = 0; j0 < live; j0 += U) {
+        if (j0 > 0) {
 #pragma unroll
-      for (int j = 0; j < ITERS; ++j) {
-        const long long t = t0 + 32 * j;
-        // the mass is read whether or not it counts, so that no load waits on a position
-        const float m = t < n ? mass[t] : 0.0f;
-        const int p = (int)key[j];
-        key[j] = t < n ? ((p < a.n_first || p > recent) ? kHeldKey : mass_key(m)) : 0u;
+          for (int u = 0; u < U; ++u) m0[u] = mass[index(j0 + u)];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int j = j0 + u;
+          if (j < live) keys[32 * j] = key_of(w0 + 32 * j + lane, (int)keys[32 * j], m0[u]);
+        }
       }
     }
-    // key of iteration j of block k (0: no token)
-    auto get = [&](int k, int j) -> unsigned {
-      if constexpr (E > 0) {
-        return key[j];
-      } else {
-        const long long t = block_at(k) + 32 * j + lane;
-        return t < n ? key_of(t, pos ? pos[t] : (int)t) : 0u;
-      }
+    // key of iteration j (0: no token)
+    auto get = [&](int j) -> unsigned {
+      if (KEEP) return keys[32 * j];
+      const int t = index(j);
+      return key_of(w0 + 32 * j + lane, pos ? pos[t] : t, mass[t]);
     };
 
     // ---- the budget-th key
     unsigned thr = 0;
     int want = a.budget;
-    bool whole = false;                  // every key equal to thr (or above, in its bin) stays
-#pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      if (whole) break;
-      const int sh = pass == 0 ? 20 : pass == 1 ? 10 : 0;
-      int* hist = pass == 0 ? s_h0 : pass == 1 ? s_h1 : s_h2;
-      const unsigned above = pass == 0 ? 0u : thr >> (sh + 10);
-      for (int k = 0; k < blocks; ++k) {
-#pragma unroll
-        for (int j = 0; j < ITERS; ++j) {
-          const unsigned u = get(k, j);
-          if (pass == 0) {
-            const unsigned bin = u >> 20;
-            // many equal masses (zeros): one count for the warp
-            if (__all_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, 0) && u != 0u)) {
-              if (lane == 0) atomicAdd(&hist[bin], 32);
-            } else if (u != 0u) {
-              atomicAdd(&hist[bin], 1);
-            }
-          } else if (u != 0u && (u >> (sh + 10)) == above) {
-            atomicAdd(&hist[(u >> sh) & 1023u], 1);
+    bool whole = false;                  // every key of the last bin stays
+#pragma unroll 1
+    for (int pass = 0; pass < 3 && !whole; ++pass) {
+      const int sh = pass == 0 ? 20 : pass == 1 ? 10 : 0, groups = pass == 0 ? 128 : 32;
+      int* hist = s_hist + (pass == 0 ? 0 : 4096 + (pass - 1) * 1024);
+      if (pass == 0) {
+#pragma unroll 4
+        for (int j = 0; j < live; ++j) {
+          const unsigned u = get(j), bin = u >> 20;
+          // many equal masses (zeros): one count for the warp
+          const unsigned first = __shfl_sync(0xffffffffu, bin, 0);
+          if (__all_sync(0xffffffffu, bin == first && u != 0u)) {
+            if (lane == 0) atomicAdd(&hist[bin], 32);
+          } else if (u != 0u) {
+            atomicAdd(&hist[bin], 1);
           }
         }
+      } else {
+        const unsigned above = thr >> (sh + 10);
+#pragma unroll 4
+        for (int j = 0; j < live; ++j) {
+          const unsigned u = get(j);
+          if (u != 0u && (u >> (sh + 10)) == above) atomicAdd(&hist[(u >> sh) & 1023u], 1);
+        }
+      }
+      __syncthreads();
+      if (tid < groups * 8) {            // eight lanes a group
+        const int4 v = reinterpret_cast<const int4*>(hist)[tid];
+        int c = (v.x + v.y) + (v.z + v.w);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+        if ((lane & 7) == 0) s_group[pass][tid >> 3] = c;
       }
       if (cs > 1) cluster_sync(); else __syncthreads();
-      // counts from the top: thread t has bins 4 (1023 - t) .. + 3, or bin 1023 - t
-      int c[4] = {0, 0, 0, 0};
-      if (pass == 0) {
-        const int at = 4 * (kEvThreads - 1 - tid);
-        for (int r = 0; r < cs; ++r) {
-          const int4 v = cs > 1 ? peer_int4(&hist[at], r) : *reinterpret_cast<const int4*>(&hist[at]);
-          c[0] += v.w; c[1] += v.z; c[2] += v.y; c[3] += v.x;
+      if (cs > 1) {
+        if (tid < groups * 8) {          // lane & 7 = rank
+          int c = (lane & 7) < cs ? peer_int(&s_group[pass][tid >> 3], lane & 7) : 0;
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+          if ((lane & 7) == 0) s_gsum[tid >> 3] = c;
         }
-      } else {
-        const int at = kEvThreads - 1 - tid;
-        for (int r = 0; r < cs; ++r) c[0] += cs > 1 ? peer_int(&hist[at], r) : hist[at];
+        __syncthreads();
       }
-      const int mine = c[0] + c[1] + c[2] + c[3];
-      int upto = warp_inclusive(mine, lane);
-      if (lane == 31) s_scan[warp] = upto;
-      __syncthreads();
-      upto += __reduce_add_sync(0xffffffffu, lane < warp ? s_scan[lane] : 0);
-      int before = upto - mine;
-      if (before < want && want <= upto) {  // one thread
-        int q = 0;
-        while (before + c[q] < want) before += c[q++];
-        s_pick[0] = pass == 0 ? 4 * (kEvThreads - 1 - tid) + 3 - q : kEvThreads - 1 - tid;
-        s_pick[1] = want - before;
-        s_pick[2] = c[q];
+      // every warp for itself: the group, counted from the top
+      const int* gs = cs > 1 ? s_gsum : s_group[pass];
+      int c[4] = {0, 0, 0, 0}, group = 0, before = 0;
+      const int per = groups / 32, top = groups - 1 - per * lane;  // this lane's first group
+      for (int q = 0; q < per; ++q) c[q] = gs[top - q];
+      const int mine = (c[0] + c[1]) + (c[2] + c[3]), upto = warp_inclusive(mine, lane);
+      {
+        const unsigned hit = __ballot_sync(0xffffffffu, upto >= want);  // not empty: want of them exist
+        const int l = __ffs(hit) - 1;
+        int q = 0, at = upto - mine;
+        while (q < per - 1 && at + c[q] < want) at += c[q++];
+        group = __shfl_sync(0xffffffffu, top - q, l);
+        before = __shfl_sync(0xffffffffu, at, l);
       }
-      __syncthreads();
-      thr |= (unsigned)s_pick[0] << sh;
-      want = s_pick[1];
-      whole = want == s_pick[2];
+      // its 32 bins
+      if (cs > 1) {
+        if (tid < 256) {
+          int v = (lane & 7) < cs ? peer_int(&hist[group * 32 + (tid >> 3)], lane & 7) : 0;
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if ((lane & 7) == 0) s_bsum[tid >> 3] = v;
+        }
+        __syncthreads();
+      }
+      const int v = cs > 1 ? s_bsum[31 - lane] : hist[group * 32 + 31 - lane];
+      const int sum = before + warp_inclusive(v, lane);
+      const int l = __ffs(__ballot_sync(0xffffffffu, sum >= want)) - 1;
+      thr |= (unsigned)(group * 32 + 31 - l) << sh;
+      const int upper = __shfl_sync(0xffffffffu, sum, l);
+      want -= upper - __shfl_sync(0xffffffffu, v, l);
+      whole = want == __shfl_sync(0xffffffffu, v, l);
     }
 
     // ---- keep words; equal keys beyond `want` leave from the highest index down
     int tie_left = 0;                    // equal keys that may stay, from this warp on
     if (!whole) {
       int ties = 0;
-      for (int k = 0; k < blocks; ++k) {
-#pragma unroll
-        for (int j = 0; j < ITERS; ++j) ties += __popc(__ballot_sync(0xffffffffu, get(k, j) == thr));
-      }
+      for (int j = 0; j < live; ++j) ties += __popc(__ballot_sync(0xffffffffu, get(j) == thr));
       if (lane == 0) s_wt[0][warp] = ties;
       __syncthreads();
       const int t = s_wt[0][lane];
@@ -241,17 +255,18 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int blocks) {
         const int all = __reduce_add_sync(0xffffffffu, t);
         if (tid == 0) s_ct[1] = all;
         cluster_sync();
-        for (unsigned r = 0; r < rank; ++r) before += peer_int(&s_ct[1], r);
+        before += __reduce_add_sync(0xffffffffu, lane < rank ? peer_int(&s_ct[1], lane) : 0);
       }
       tie_left = max(0, want - before);
     }
-    // this lane's word of block k: bit i = token block_at(k) + 32 lane + i
+    // this lane's word of iterations j0 .. j0 + 31: bit i = token w0 + 32 (j0 + lane) + i
     int tie_run = tie_left;
-    auto keep_word = [&](int k) {
+    auto keep_word = [&](int j0) {
+      const int nj = min(32, live - j0);
       unsigned w = 0u, tw = 0u;
-#pragma unroll
-      for (int j = 0; j < ITERS; ++j) {
-        const unsigned u = get(k, j);
+#pragma unroll 4
+      for (int j = 0; j < nj; ++j) {
+        const unsigned u = get(j0 + j);
         const unsigned kw = __ballot_sync(0xffffffffu, whole ? u >= thr : u > thr);
         if (lane == j) w = kw;
         if (!whole) {
@@ -261,29 +276,26 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int blocks) {
       }
       if (!whole) {
         const int c = __popc(tw), upto = warp_inclusive(c, lane);
-        int stay = min(c, max(0, tie_run - (upto - c)));
+        const int stay = min(c, max(0, tie_run - (upto - c)));
         tie_run = max(0, tie_run - __shfl_sync(0xffffffffu, upto, 31));
-        unsigned t = tw;
-        for (int drop = c - stay; drop > 0; --drop) t &= ~(0x80000000u >> __clz(t));
-        w |= t;
+        for (int drop = c - stay; drop > 0; --drop) tw &= ~(0x80000000u >> __clz(tw));
+        w |= tw;
       }
       return w;
     };
-    // tokens of the word before `limit`, as a mask
-    auto below = [&](long long t0, long long limit) {
-      const long long m = limit - t0;
+    // this lane's tokens before the budget, as a mask
+    auto front_word = [&](int j0) {
+      const long long m = j0 + lane < live ? a.budget - (w0 + 32 * (j0 + lane)) : 0;
       return m <= 0 ? 0u : m >= 32 ? 0xffffffffu : (1u << (int)m) - 1u;
     };
     unsigned word = 0u;
     int holes = 0, fills = 0;
-    for (int k = 0; k < blocks; ++k) {
-      word = keep_word(k);
-      const long long t0 = block_at(k) + 32 * lane;
-      const unsigned front = lane < ITERS ? below(t0, a.budget) : 0u;
+    for (int j0 = 0; j0 < live; j0 += 32) {
+      word = keep_word(j0);
+      const unsigned front = front_word(j0);
       holes += __popc(~word & front);    // budget < n: every token before it exists
-      fills += __popc(lane < ITERS ? word & ~front : 0u);
+      fills += __popc(word & ~front);
     }
-    const int lane_holes = holes, lane_fills = fills;
     holes = __reduce_add_sync(0xffffffffu, holes);
     fills = __reduce_add_sync(0xffffffffu, fills);
     if (lane == 0) { s_wt[1][warp] = holes; s_wt[2][warp] = fills; }
@@ -296,27 +308,38 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int blocks) {
       const int all_h = __reduce_add_sync(0xffffffffu, th);
       if (tid == 0) { s_ct[2] = all_h; s_ct[3] = moves; }
       cluster_sync();
-      moves = 0;
-      for (int r = 0; r < cs; ++r) {
-        const int f = peer_int(&s_ct[3], r);
-        moves += f;
-        if (r < (int)rank) { hole_at += peer_int(&s_ct[2], r); fill_at += f; }
-      }
+      const int f = lane < cs ? peer_int(&s_ct[3], lane) : 0;
+      const int h = lane < rank ? peer_int(&s_ct[2], lane) : 0;
+      moves = __reduce_add_sync(0xffffffffu, f);
+      hole_at += __reduce_add_sync(0xffffffffu, h);
+      fill_at += __reduce_add_sync(0xffffffffu, lane < rank ? f : 0);
     }
     tie_run = tie_left;
-    for (int k = 0; k < blocks; ++k) {
-      if (blocks > 1) word = keep_word(k);
-      const long long t0 = block_at(k) + 32 * lane;
-      const unsigned front = lane < ITERS ? below(t0, a.budget) : 0u;
-      unsigned hw = ~word & front, fw = lane < ITERS ? word & ~front : 0u;
-      const int ch = blocks > 1 ? __popc(hw) : lane_holes, cf = blocks > 1 ? __popc(fw) : lane_fills;
-      const int uh = warp_inclusive(ch, lane), uf = warp_inclusive(cf, lane);
-      int32_t* h = hole + hole_at + uh - ch;
-      for (; hw; hw &= hw - 1) *h++ = (int32_t)(t0 + __ffs(hw) - 1);
-      int32_t* f = fill + fill_at + uf - cf;
-      for (; fw; fw &= fw - 1) *f++ = (int32_t)(t0 + __ffs(fw) - 1);
-      hole_at += __shfl_sync(0xffffffffu, uh, 31);
-      fill_at += __shfl_sync(0xffffffffu, uf, 31);
+    // Lists the set bits of the lanes' words in order, from list[at] on: word
+    // by word, so that neighbours are written together, or each lane its own
+    // when no word is crowded.
+    auto list = [&](unsigned w, int32_t* out, int at, int j0) {
+      const int c = __popc(w), upto = warp_inclusive(c, lane);
+      if (__reduce_max_sync(0xffffffffu, c) <= 12) {
+        int32_t* o = out + at + upto - c;
+        const int t0 = (int)(w0 + 32 * (j0 + lane));
+        for (; w; w &= w - 1) *o++ = t0 + __ffs(w) - 1;
+      } else {
+        const unsigned bit = 1u << lane;
+        for (unsigned some = __ballot_sync(0xffffffffu, w != 0u); some; some &= some - 1) {
+          const int j = __ffs(some) - 1;
+          const unsigned v = __shfl_sync(0xffffffffu, w, j);
+          const int o = at + __shfl_sync(0xffffffffu, upto - c, j);
+          if (v & bit) out[o + __popc(v & (bit - 1))] = (int)(w0 + 32 * (j0 + j)) + lane;
+        }
+      }
+      return at + __shfl_sync(0xffffffffu, upto, 31);
+    };
+    for (int j0 = 0; j0 < live; j0 += 32) {
+      if (live > 32) word = keep_word(j0);
+      const unsigned front = front_word(j0);
+      hole_at = list(~word & front, hole, hole_at, j0);
+      fill_at = list(word & ~front, fill, fill_at, j0);
     }
     if (cs > 1) cluster_sync();          // no CTA leaves while its counts are read
   }
@@ -396,11 +419,16 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, int groups, long lon
   }
 }
 
-template <int E>
-cudaError_t run_evict(const EvictArgs& a, int cs, int blocks, cudaStream_t st) {
+template <bool KEEP>
+cudaError_t run_evict(const EvictArgs& a, int cs, size_t smem, cudaStream_t st) {
+  auto kern = evict_select_kernel<KEEP>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kKeepTokens * kEvThreads * 4);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.s.batch * a.n_mass) * cs);
   cfg.blockDim = dim3(kEvThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -410,7 +438,7 @@ cudaError_t run_evict(const EvictArgs& a, int cs, int blocks, cudaStream_t st) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<E>, a, cs, blocks);
+  return cudaLaunchKernelEx(&cfg, kern, a, cs);
 }
 
 }  // namespace
@@ -421,16 +449,12 @@ cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st) {
   const long long rows = (long long)a.s.batch * a.n_mass, L = a.s.L_ctx;
   const int sms = tc_sm_count();
   int cs = 1;
-  while (cs < kMaxCluster && ((rows * cs * 2 <= sms && L > (long long)cs * 1024) ||
-                              L > (long long)cs * kRegTokens * kEvThreads))
+  while (cs < kMaxCluster && ((rows * cs * 2 <= sms && L > (long long)cs * kEvThreads) ||
+                              L > (long long)cs * kKeepTokens * kEvThreads))
     cs *= 2;
-  const long long per = (L + (long long)cs * kEvThreads - 1) / ((long long)cs * kEvThreads);
-  if (per <= 2) return run_evict<2>(a, cs, 1, st);
-  if (per <= 4) return run_evict<4>(a, cs, 1, st);
-  if (per <= 8) return run_evict<8>(a, cs, 1, st);
-  if (per <= 16) return run_evict<16>(a, cs, 1, st);
-  if (per <= kRegTokens) return run_evict<32>(a, cs, 1, st);
-  return run_evict<0>(a, cs, (int)((per + 31) / 32), st);
+  const long long it = (L + (long long)cs * kEvThreads - 1) / ((long long)cs * kEvThreads);
+  if (it <= kKeepTokens) return run_evict<true>(a, cs, (size_t)it * kEvThreads * 4, st);
+  return run_evict<false>(a, cs, 0, st);
 }
 
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {

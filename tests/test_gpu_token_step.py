@@ -388,6 +388,10 @@ EVICT_CASES = [
     (100, [100, 50], 2, 100, 10, 10, False, "random"),   # budget = capacity: no moves at all
     (40000, [40000, 12345], 1, 5000, 4, 300, True, "random"),
     (130001, [130001], 1, 65000, 0, 0, False, "ties"),
+    (420001, [420001, 400000], 1, 100000, 4, 1000, True, "random"),   # keys not kept on chip
+    (400000, [400000], 1, 90000, 0, 0, False, "ties"),
+    (300001, [300001], 1, 150000, 0, 9, True, "ties"),                  # 37 iterations a warp
+    (1500, [1500] * 90 + [900, 1200], 2, 800, 2, 16, False, "random"),  # more rows than SMs
 ]
 
 
