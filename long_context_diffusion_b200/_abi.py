@@ -261,30 +261,44 @@ def dl_block_scores_noalloc(desc, Q_dec, q_idx, q_cnt, Kbar, n_units, score, str
 
 # ---- one token at a time over the same cache (dl.h, c1-c4) ----
 
-class _Buffers:
-    """Buffer checks of one call: every tensor contiguous, of the stated type
-    and number of elements, all on one device, which must be the current one
-    (the call launches there).  Returns the data pointers."""
+# The current stream of a device as its raw handle: a tenth of the cost of
+# building a torch.cuda.Stream, which counts in calls of a few microseconds.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-    def __init__(self, name: str):
-        self.name, self.dev = name, torch.cuda.current_device() if torch.cuda.is_available() else -1
 
-    def __call__(self, t, what: str, dtype, n: int):
-        if t is None:
-            return None
-        if t.dtype is not dtype or t.numel() != n or t.get_device() != self.dev or \
-                self.dev < 0 or not t.is_contiguous():
-            raise ValueError(
-                f"{self.name}: {what} must be a contiguous {dtype} tensor of {n} elements on the "
-                f"current CUDA device ({self.dev}), got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _device_of(name: str, t: torch.Tensor) -> int:
+    """The device a call launches on: that of its buffers, which must be the
+    current one."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{name}: buffers must be on the current CUDA device, got {t.device}")
+    return dev
+
+
+def _buf(t, dtype, n: int, dev: int, what: str):
+    """Data pointer of a call's buffer (None: NULL) of n elements of dtype on
+    device dev."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
+    raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements on the current CUDA "
+                     f"device ({dev}), got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _stream(stream, dev: int):
+    return _current_raw_stream(dev) if stream is None else _s(stream)
+
+
+_I32, _F32 = torch.int32, torch.float32
 
 
 def _dtype_of(desc):
     return torch.bfloat16 if desc.dtype == DL_BF16 else torch.float32
 
 
-def _mass_rows(name, desc, *arrays):
+def _mass_rows(name, *arrays):
     """Rows per sequence of the per-token arrays [batch][n_mass][...]."""
     for t in arrays:
         if t is not None:
@@ -303,83 +317,89 @@ def dl_qk_norm_rope(desc, qkv, pos, q_weight, k_weight, eps, inv_freq, Q_out, K_
     inv_freq None: no rotation.  Outputs: Q_out, and K_out/V_out and/or the
     cache (start, page_table, K_pool, V_pool, with end, tok_pos, tok_mass)."""
     B, H, H_kv, d = desc.batch, desc.H, desc.H_kv, desc.d
-    name, dt, buf = "dl_qk_norm_rope", _dtype_of(desc), _Buffers("dl_qk_norm_rope")
-    if qkv.dim() != 3 or qkv.shape[0] != B or qkv.dtype is not dt or \
-            qkv.get_device() != buf.dev or buf.dev < 0:
-        raise ValueError(f"{name}: qkv must be a [{B}][n_tok][...] {dt} tensor on the current CUDA "
-                         f"device, got {qkv.dtype} {tuple(qkv.shape)} on {qkv.device}")
-    n = qkv.shape[1]
-    s0, stride, s2 = qkv.stride()
+    dt, dev = _dtype_of(desc), _device_of("dl_qk_norm_rope", qkv)
+    width = (H + 2 * H_kv) * d
+    if qkv.dim() != 3 or qkv.dtype is not dt:
+        raise ValueError(f"dl_qk_norm_rope: qkv must be a [batch][n_tok][...] {dt} tensor, got "
+                         f"{qkv.dtype} {tuple(qkv.shape)}")
+    (b, n, w), (s0, stride, s2) = qkv.shape, qkv.stride()
     if n == 1:
-        stride = s0 if B > 1 else max(stride, qkv.shape[2])
-    if s2 != 1 or (B > 1 and n > 1 and s0 != n * stride) or stride < qkv.shape[2] or \
-            qkv.shape[2] < (H + 2 * H_kv) * d:
-        raise ValueError(f"{name}: qkv rows must hold (H + 2 H_kv) d = {(H + 2 * H_kv) * d} values "
-                         f"with unit stride and equal steps between tokens, got shape "
-                         f"{tuple(qkv.shape)} strides {qkv.stride()}")
+        stride = s0 if B > 1 else max(stride, w)
+    if b != B or s2 != 1 or w < width or stride < w or (B > 1 and n > 1 and s0 != n * stride):
+        raise ValueError(f"dl_qk_norm_rope: qkv must hold {B} sequences whose token rows have "
+                         f"(H + 2 H_kv) d = {width} values with unit stride and equal steps between "
+                         f"tokens, got shape {tuple(qkv.shape)} strides {qkv.stride()}")
+    rows = B * n * d
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    n_mass = _mass_rows(name, desc, tok_pos, tok_mass)
-    rows, pool, book = B * n * d, desc.n_slots * H_kv * desc.page * d, B * n_mass * desc.L_ctx
-    i32, f32 = torch.int32, torch.float32
+    n_mass = start_p = table_p = kp = vp = end_p = tp = tm = None
+    if start is not None:
+        pool = desc.n_slots * H_kv * desc.page * d
+        n_mass = _mass_rows("dl_qk_norm_rope", tok_pos, tok_mass)
+        book = B * n_mass * desc.L_ctx
+        start_p = _buf(start, _I32, B, dev, "start")
+        table_p = _buf(page_table, _I32, B * desc.n_pages, dev, "page_table")
+        kp, vp = _buf(K_pool, dt, pool, dev, "K_pool"), _buf(V_pool, dt, pool, dev, "V_pool")
+        end_p = _buf(end, _I32, B, dev, "end")
+        tp, tm = _buf(tok_pos, _I32, book, dev, "tok_pos"), _buf(tok_mass, _F32, book, dev, "tok_mass")
+    elif not (page_table is K_pool is V_pool is end is tok_pos is tok_mass is None):
+        raise ValueError("dl_qk_norm_rope: page_table, pools, end, tok_pos and tok_mass need start")
     _check(lib.dl_qk_norm_rope(
-        ctypes.byref(desc), qkv.data_ptr(), stride, n, buf(pos, "pos", i32, B * n),
-        buf(q_weight, "q_weight", dt, d), buf(k_weight, "k_weight", dt, d), eps,
-        buf(inv_freq, "inv_freq", f32, rot // 2), rot, interleaved,
-        buf(Q_out, "Q_out", dt, rows * H), buf(K_out, "K_out", dt, rows * H_kv),
-        buf(V_out, "V_out", dt, rows * H_kv), buf(start, "start", i32, B),
-        buf(page_table, "page_table", i32, B * desc.n_pages), buf(K_pool, "K_pool", dt, pool),
-        buf(V_pool, "V_pool", dt, pool), buf(end, "end", i32, B),
-        buf(tok_pos, "tok_pos", i32, book), buf(tok_mass, "tok_mass", f32, book), n_mass,
-        _s(stream)))
+        ctypes.byref(desc), qkv.data_ptr(), stride, n, _buf(pos, _I32, B * n, dev, "pos"),
+        _buf(q_weight, dt, d, dev, "q_weight"), _buf(k_weight, dt, d, dev, "k_weight"), eps,
+        _buf(inv_freq, _F32, rot // 2, dev, "inv_freq"), rot, interleaved,
+        _buf(Q_out, dt, rows * H, dev, "Q_out"), _buf(K_out, dt, rows * H_kv, dev, "K_out"),
+        _buf(V_out, dt, rows * H_kv, dev, "V_out"), start_p, table_p, kp, vp, end_p, tp, tm,
+        n_mass or 1, _stream(stream, dev)))
 
 
 def dl_decode_attn(desc, Q, K_pool, V_pool, page_table, ctx_len, O, lse, ws, tok_mass=None,
                    decay=1.0, stream=None):
     """tok_mass [batch][1 or H_kv][L_ctx], accumulated in place (or None)."""
     B, H, d = desc.batch, desc.H, desc.d
-    name, dt, buf = "dl_decode_attn", _dtype_of(desc), _Buffers("dl_decode_attn")
-    n_mass = _mass_rows(name, desc, tok_mass)
-    pool = desc.n_slots * desc.H_kv * desc.page * d
-    if ws.get_device() != buf.dev or not ws.is_contiguous():
-        raise ValueError(f"{name}: the workspace must be contiguous on the current CUDA device")
+    dt, dev = _dtype_of(desc), _device_of("dl_decode_attn", Q)
+    pool, n_mass, mass = desc.n_slots * desc.H_kv * desc.page * d, 1, None
+    if tok_mass is not None:
+        n_mass = _mass_rows("dl_decode_attn", tok_mass)
+        mass = _buf(tok_mass, _F32, B * n_mass * desc.L_ctx, dev, "tok_mass")
     _check(lib.dl_decode_attn(
-        ctypes.byref(desc), buf(Q, "Q", dt, B * H * d), buf(K_pool, "K_pool", dt, pool),
-        buf(V_pool, "V_pool", dt, pool),
-        buf(page_table, "page_table", torch.int32, B * desc.n_pages),
-        buf(ctx_len, "ctx_len", torch.int32, B), buf(O, "O", dt, B * H * d),
-        buf(lse, "lse", torch.float32, B * H),
-        buf(tok_mass, "tok_mass", torch.float32, B * n_mass * desc.L_ctx), n_mass, decay,
-        ws.data_ptr(), ws.numel() * ws.element_size(), _s(stream)))
+        ctypes.byref(desc), _buf(Q, dt, B * H * d, dev, "Q"), _buf(K_pool, dt, pool, dev, "K_pool"),
+        _buf(V_pool, dt, pool, dev, "V_pool"),
+        _buf(page_table, _I32, B * desc.n_pages, dev, "page_table"),
+        _buf(ctx_len, _I32, B, dev, "ctx_len"), _buf(O, dt, B * H * d, dev, "O"),
+        _buf(lse, _F32, B * H, dev, "lse"), mass, n_mass, decay,
+        _buf(ws, ws.dtype, ws.numel(), dev, "ws"), ws.numel() * ws.element_size(),
+        _stream(stream, dev)))
 
 
 def dl_evict_select(desc, tok_mass, tok_pos, ctx_len, budget, n_first, n_recent, hole_idx,
                     fill_idx, move_cnt, new_len, stream=None):
     """hole_idx, fill_idx [batch][n_mass][max_move]; tok_pos may be None (the
     index is the position)."""
-    B, name, buf = desc.batch, "dl_evict_select", _Buffers("dl_evict_select")
-    n_mass = _mass_rows(name, desc, tok_mass)
+    B, dev = desc.batch, _device_of("dl_evict_select", tok_mass)
+    n_mass = _mass_rows("dl_evict_select", tok_mass)
     max_move = 0 if hole_idx is None else hole_idx.shape[-1]
-    book, moves, i32 = B * n_mass * desc.L_ctx, B * n_mass * max_move, torch.int32
+    book, moves = B * n_mass * desc.L_ctx, B * n_mass * max_move
     _check(lib.dl_evict_select(
-        ctypes.byref(desc), buf(tok_mass, "tok_mass", torch.float32, book),
-        buf(tok_pos, "tok_pos", i32, book), n_mass, buf(ctx_len, "ctx_len", i32, B), budget,
-        n_first, n_recent, buf(hole_idx, "hole_idx", i32, moves),
-        buf(fill_idx, "fill_idx", i32, moves), max_move,
-        buf(move_cnt, "move_cnt", i32, B * n_mass), buf(new_len, "new_len", i32, B), _s(stream)))
+        ctypes.byref(desc), _buf(tok_mass, _F32, book, dev, "tok_mass"),
+        _buf(tok_pos, _I32, book, dev, "tok_pos"), n_mass, _buf(ctx_len, _I32, B, dev, "ctx_len"),
+        budget, n_first, n_recent, _buf(hole_idx, _I32, moves, dev, "hole_idx"),
+        _buf(fill_idx, _I32, moves, dev, "fill_idx"), max_move,
+        _buf(move_cnt, _I32, B * n_mass, dev, "move_cnt"), _buf(new_len, _I32, B, dev, "new_len"),
+        _stream(stream, dev)))
 
 
 def dl_cache_compact(desc, hole_idx, fill_idx, move_cnt, page_table, K_pool, V_pool, tok_pos=None,
                      tok_mass=None, stream=None):
     """The moves of dl_evict_select's lists ([batch][n_mass][max_move])."""
-    B, name, buf = desc.batch, "dl_cache_compact", _Buffers("dl_cache_compact")
-    n_mass = _mass_rows(name, desc, hole_idx)
-    max_move, dt, i32 = hole_idx.shape[-1], _dtype_of(desc), torch.int32
-    pool = desc.n_slots * desc.H_kv * desc.page * desc.d
+    B, dev, dt = desc.batch, _device_of("dl_cache_compact", K_pool), _dtype_of(desc)
+    n_mass = _mass_rows("dl_cache_compact", hole_idx)
+    max_move, pool = hole_idx.shape[-1], desc.n_slots * desc.H_kv * desc.page * desc.d
     book, moves = B * n_mass * desc.L_ctx, B * n_mass * max_move
     _check(lib.dl_cache_compact(
-        ctypes.byref(desc), buf(hole_idx, "hole_idx", i32, moves),
-        buf(fill_idx, "fill_idx", i32, moves), buf(move_cnt, "move_cnt", i32, B * n_mass), max_move,
-        n_mass, buf(page_table, "page_table", i32, B * desc.n_pages),
-        buf(K_pool, "K_pool", dt, pool), buf(V_pool, "V_pool", dt, pool),
-        buf(tok_pos, "tok_pos", i32, book), buf(tok_mass, "tok_mass", torch.float32, book),
-        _s(stream)))
+        ctypes.byref(desc), _buf(hole_idx, _I32, moves, dev, "hole_idx"),
+        _buf(fill_idx, _I32, moves, dev, "fill_idx"),
+        _buf(move_cnt, _I32, B * n_mass, dev, "move_cnt"), max_move, n_mass,
+        _buf(page_table, _I32, B * desc.n_pages, dev, "page_table"),
+        _buf(K_pool, dt, pool, dev, "K_pool"), _buf(V_pool, dt, pool, dev, "V_pool"),
+        _buf(tok_pos, _I32, book, dev, "tok_pos"), _buf(tok_mass, _F32, book, dev, "tok_mass"),
+        _stream(stream, dev)))

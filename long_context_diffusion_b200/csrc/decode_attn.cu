@@ -876,7 +876,7 @@ cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
                                 tc_map_f32_2d(&mv, a.Vp, D, rows, C::KT);
   if (!ok) return cudaErrorInvalidValue;
   auto kern = decode_kernel<T, D, RB>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = allow_smem<decode_kernel<T, D, RB>>(C::SMEM);
   if (e != cudaSuccess) return e;
   const long long most = (long long)s.batch * items_per_seq(s) * ((s.L_ctx + C::KT - 1) / C::KT);
   int P = tc_sm_count() * kCtasPerSm;

@@ -4,11 +4,13 @@
 // in the order of its bits (held tokens at +infinity, NaN at -infinity),
 // equal keys by the lower index.
 //
-// Bound: latency (a row of n tokens is 8 n bytes; 128 rows of 32K, 38 MB, are
-// 6 us of HBM).  A decision row is taken by a cluster of 1 to 8 CTAs that
-// splits its n tokens evenly in index order and keeps their keys in shared
-// memory, so that masses and positions are read once; a warp owns 32 it
-// consecutive tokens, lane l of iteration j having token 32 j + l.
+// Bound: latency and instruction issue (a row of n tokens is 8 n bytes; 128
+// rows of 32K, 38 MB, are 6 us of HBM; every instruction a token takes is 1 us
+// there, so tokens are handled four at a time where they can be).  A decision
+// row is taken by a cluster of 1 to 8 CTAs that splits its n tokens evenly in
+// index order.  A warp reads its tokens coalesced, 16 bytes a lane, and turns
+// them through shared memory so that each lane ends with `it` consecutive
+// tokens; their keys stay there, masses and positions are read once.
 //  - The budget-th key by radix select: a histogram of the top 12 bits (sign,
 //    exponent, three bits of mantissa), then of the next 10 and the last 10
 //    among the keys that share the digits found.  Each CTA counts its own
@@ -16,11 +18,10 @@
 //    sums over the cluster, finds the group, and adds that group's 32 bins
 //    alone (adding all bins over the cluster took four times as long).  The
 //    search ends at the first digit whose whole bin stays.
-//  - One vote per iteration gives the 32 tokens' keep bits as a word, lane j
-//    holding iteration j's; holes and fills are then counted and listed by
-//    words, with prefix sums over lanes, warps and CTAs.
-// Rows too long for the cluster's shared memory (KEEP false) recompute their
-// keys from memory in every pass.
+//  - A lane's keep bits are one word; holes and fills are counted and listed
+//    by words, with prefix sums over lanes, warps and CTAs.
+// Rows too long for the cluster's shared memory go through it in tiles, read
+// again for every pass.
 //
 // Moves: bound by HBM (each moved row is read and written once).  A warp
 // resolves 32 moves at a time, one per lane, then all lanes copy their rows in
@@ -37,7 +38,7 @@ namespace {
 constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kKeepTokens = 48;          // most tokens of a thread kept in shared memory (192 KB)
+constexpr int kMaxIt = 44;               // most tokens of a thread: 11 16-byte chunks, 176 KB a CTA
 constexpr unsigned kHeldKey = 0xFF800000u;  // the key of +infinity
 
 // Order-preserving bits of a mass: a < b as numbers <=> key(a) < key(b);
@@ -74,11 +75,33 @@ __device__ __forceinline__ int warp_inclusive(int v, int lane) {
   return v;
 }
 
-// KEEP: keys in shared memory; else recomputed from memory.
-template <bool KEEP>
+// Lists the set bits of the lanes' words, in order, from out[at] on; bit i of
+// lane l is token t0 + i of that lane.  Word by word, so that neighbours are
+// written together, or each lane its own when no word is crowded.
+__device__ __forceinline__ int list_bits(unsigned long long w, int32_t* out, int at, long long t0,
+                                         int it, int lane) {
+  const int c = __popcll(w), upto = warp_inclusive(c, lane);
+  if (__reduce_max_sync(0xffffffffu, c) <= 12) {
+    int32_t* o = out + at + upto - c;
+    for (; w; w &= w - 1) *o++ = (int32_t)(t0 + __ffsll(w) - 1);
+  } else {
+    for (unsigned some = __ballot_sync(0xffffffffu, w != 0ull); some; some &= some - 1) {
+      const int j = __ffs(some) - 1;
+      const unsigned long long v = __shfl_sync(0xffffffffu, w, j);
+      const int o = at + __shfl_sync(0xffffffffu, upto - c, j);
+      const long long t = __shfl_sync(0xffffffffu, t0, j);
+      for (int i = lane; i < it; i += 32)
+        if ((v >> i) & 1) out[o + __popcll(v & ((1ull << i) - 1))] = (int32_t)(t + i);
+    }
+  }
+  return at + __shfl_sync(0xffffffffu, upto, 31);
+}
+
+// VEC: masses and positions may be read 16 bytes at a time.
+template <bool VEC>
 __global__ void __launch_bounds__(kEvThreads, 1)
-evict_select_kernel(const __grid_constant__ EvictArgs a, int cs) {
-  extern __shared__ unsigned s_key[];
+evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int max_it) {
+  extern __shared__ uint4 s_key[];       // [thread][it / 4 | 1]
   __shared__ __align__(16) int s_hist[4096 + 2 * 1024];
   __shared__ int s_group[3][128];        // this CTA's counts of 32 bins
   __shared__ int s_gsum[128], s_bsum[32];  // the cluster's
@@ -104,29 +127,73 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs) {
   if (!bad && n > a.budget) {            // the same for the whole cluster
     const float* mass = a.tok_mass + (size_t)row * s.L_ctx;
     const int32_t* pos = a.tok_pos ? a.tok_pos + (size_t)row * s.L_ctx : nullptr;
-    // this warp's tokens [w0, w0 + 32 it) (those below n exist); 64-bit: the
-    // last warps' may lie past 2^31
-    const int it = (int)(((long long)n + cs * kEvThreads - 1) / (cs * kEvThreads));
-    const long long w0 = ((long long)rank * kEvWarps + warp) * 32 * it;
-    const int live = (int)max(0ll, min((long long)it, ((long long)n - w0 + 31) / 32));  // iterations
-    unsigned* keys = s_key + warp * 32 * it + lane;
-    // Loads are unconditional (indices clamped to the row), so that a thread's
-    // are all in flight together; the first masses do not wait for the largest
-    // position.
-    constexpr int U = 8;
-    auto index = [&](int j) { return (int)min(w0 + 32 * j + lane, (long long)n - 1); };
-    float m0[U];
+    // Tokens per thread of a tile, a multiple of 4; tiles; the tile's first
+    // token of this warp.  64 bits: the last ones may lie past 2^31.
+    const int span = cs * kEvThreads;
+    int it = (int)(((long long)n + 4 * span - 1) / (4 * span)) * 4, tiles = 1;
+    if (it > max_it) {
+      tiles = (it + max_it - 1) / max_it;
+      it = max_it;
+    }
+    const int cpl = it / 4, pitch = cpl | 1;  // chunks of a lane; an odd pitch spreads the banks
+    uint4* warp_keys = s_key + warp * 32 * pitch;
+    uint4* my_keys = warp_keys + lane * pitch;
+    auto warp_at = [&](int k) {
+      return (((long long)rank * tiles + k) * kEvWarps + warp) * 32 * it;
+    };
+    // chunk q (16 bytes) of a warp's tile belongs to lane q / cpl
+    const int step_l = 32 / cpl, step_c = 32 % cpl;
+    struct Spot { int l, c; };
+    auto first_spot = [&]() { return Spot{lane / cpl, lane % cpl}; };
+    auto next_spot = [&](Spot& p) {
+      p.l += step_l;
+      p.c += step_c;
+      if (p.c >= cpl) { p.c -= cpl; ++p.l; }
+    };
+    // four values at token t (a chunk behind the row's end repeats its last)
+    auto load4 = [&](const int* x, long long t) -> int4 {
+      if (VEC) return *reinterpret_cast<const int4*>(x + min(t, (long long)((n - 1) & ~3)));
+      int4 v;
+      v.x = x[min(t, (long long)n - 1)];
+      v.y = x[min(t + 1, (long long)n - 1)];
+      v.z = x[min(t + 2, (long long)n - 1)];
+      v.w = x[min(t + 3, (long long)n - 1)];
+      return v;
+    };
+    auto load_pos = [&](long long t) -> int4 {
+      return pos ? load4(pos, t) : make_int4((int)t, (int)t + 1, (int)t + 2, (int)t + 3);
+    };
+    const int* massi = reinterpret_cast<const int*>(mass);
+    constexpr int U = 4;                 // 16-byte loads ahead
+    int4 m0[U];                          // the first masses do not wait for the largest position
+    if (tiles == 1) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) m0[u] = mass[index(u)];
+      for (int u = 0; u < U; ++u) m0[u] = load4(massi, warp_at(0) + 4 * (32 * u + lane));
+    }
     int last = INT32_MIN;
-    for (int j0 = 0; j0 < live; j0 += U) {
-      int p[U];
+    for (int k = 0; k < tiles; ++k) {
+      const long long t0 = warp_at(k) + 4 * lane;
+      Spot sp = first_spot();
+      for (int i0 = 0; i0 < cpl; i0 += U) {
+        if (warp_at(k) + 128 * i0 >= n) break;
+        int4 p[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) p[u] = pos ? pos[index(j0 + u)] : index(j0 + u);
+        for (int u = 0; u < U; ++u) p[u] = load_pos(t0 + 128 * (i0 + u));
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        last = max(last, p[u]);          // a clamped index repeats a token of the row
-        if (KEEP && j0 + u < live) keys[32 * (j0 + u)] = (unsigned)p[u];
+        for (int u = 0; u < U; ++u) {
+          const long long t = t0 + 128 * (i0 + u);
+          if (t + 3 < n) {
+            last = max(max(max(last, p[u].x), max(p[u].y, p[u].z)), p[u].w);
+          } else {
+            if (t < n) last = max(last, p[u].x);
+            if (t + 1 < n) last = max(last, p[u].y);
+            if (t + 2 < n) last = max(last, p[u].z);
+          }
+          if (tiles == 1 && i0 + u < cpl) {
+            warp_keys[sp.l * pitch + sp.c] = make_uint4(p[u].x, p[u].y, p[u].z, p[u].w);
+            next_spot(sp);
+          }
+        }
       }
     }
     last = __reduce_max_sync(0xffffffffu, last);
@@ -138,30 +205,50 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs) {
       cluster_sync();
       last = __reduce_max_sync(0xffffffffu, lane < cs ? peer_int(&s_ct[0], lane) : INT32_MIN);
     }
-    const long long recent = (long long)last - a.n_recent;
-    auto key_of = [&](long long t, int p, float m) {
-      return t >= n ? 0u : (p < a.n_first || p > recent) ? kHeldKey : mass_key(m);
+    // not held: n_first <= pos <= last - n_recent, as one unsigned comparison
+    const long long room = (long long)last - a.n_recent - a.n_first + 1;
+    const unsigned loose = room > 0 ? (unsigned)min(room, 0xffffffffll) : 0u;
+    auto key_of = [&](int p, int m) {
+      return (unsigned)p - (unsigned)a.n_first < loose ? mass_key(__int_as_float(m)) : kHeldKey;
     };
-    if (KEEP) {
+    // Keys of tile k, each lane's own chunks in order (0: no token).
+    auto load_tile = [&](int k) {
+      const long long t0 = warp_at(k) + 4 * lane;
+      Spot sp = first_spot();
+      __syncwarp();
 #pragma unroll 1
-      for (int j0 = 0; j0 < live; j0 += U) {
-        if (j0 > 0) {
+      for (int i0 = 0; i0 < cpl; i0 += U) {
+        const bool none = warp_at(k) + 128 * i0 >= n;  // nothing here for the warp
+        if (!none && (i0 > 0 || tiles > 1)) {
 #pragma unroll
-          for (int u = 0; u < U; ++u) m0[u] = mass[index(j0 + u)];
+          for (int u = 0; u < U; ++u) m0[u] = load4(massi, t0 + 128 * (i0 + u));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int j = j0 + u;
-          if (j < live) keys[32 * j] = key_of(w0 + 32 * j + lane, (int)keys[32 * j], m0[u]);
+          if (i0 + u >= cpl) break;
+          const long long t = t0 + 128 * (i0 + u);
+          uint4* at = warp_keys + sp.l * pitch + sp.c;
+          uint4 q = make_uint4(0u, 0u, 0u, 0u);
+          if (t < n) {
+            int4 p;
+            if (tiles == 1) {
+              const uint4 v = *at;
+              p = make_int4(v.x, v.y, v.z, v.w);
+            } else {
+              p = load_pos(t);
+            }
+            q.x = key_of(p.x, m0[u].x);
+            if (t + 1 < n) q.y = key_of(p.y, m0[u].y);
+            if (t + 2 < n) q.z = key_of(p.z, m0[u].z);
+            if (t + 3 < n) q.w = key_of(p.w, m0[u].w);
+          }
+          *at = q;
+          next_spot(sp);
         }
       }
-    }
-    // key of iteration j (0: no token)
-    auto get = [&](int j) -> unsigned {
-      if (KEEP) return keys[32 * j];
-      const int t = index(j);
-      return key_of(w0 + 32 * j + lane, pos ? pos[t] : t, mass[t]);
+      __syncwarp();
     };
+    if (tiles == 1) load_tile(0);
 
     // ---- the budget-th key
     unsigned thr = 0;
@@ -171,24 +258,34 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs) {
     for (int pass = 0; pass < 3 && !whole; ++pass) {
       const int sh = pass == 0 ? 20 : pass == 1 ? 10 : 0, groups = pass == 0 ? 128 : 32;
       int* hist = s_hist + (pass == 0 ? 0 : 4096 + (pass - 1) * 1024);
-      if (pass == 0) {
-#pragma unroll 4
-        for (int j = 0; j < live; ++j) {
-          const unsigned u = get(j), bin = u >> 20;
-          // many equal masses (zeros): one count for the warp
-          const unsigned first = __shfl_sync(0xffffffffu, bin, 0);
-          if (__all_sync(0xffffffffu, bin == first && u != 0u)) {
-            if (lane == 0) atomicAdd(&hist[bin], 32);
-          } else if (u != 0u) {
-            atomicAdd(&hist[bin], 1);
+      for (int k = 0; k < tiles; ++k) {
+        if (tiles > 1) load_tile(k);
+        if (warp_at(k) >= n) break;
+        if (pass == 0) {
+          for (int c = 0; c < cpl; ++c) {
+            const uint4 q = my_keys[c];
+            const unsigned first = __shfl_sync(0xffffffffu, q.x, 0) >> 20;
+            // many equal masses (zeros): one count for the warp
+            if (__all_sync(0xffffffffu, q.w != 0u && (q.x >> 20) == first && (q.y >> 20) == first &&
+                                            (q.z >> 20) == first && (q.w >> 20) == first)) {
+              if (lane == 0) atomicAdd(&hist[first], 128);
+            } else {
+              if (q.x) atomicAdd(&hist[q.x >> 20], 1);
+              if (q.y) atomicAdd(&hist[q.y >> 20], 1);
+              if (q.z) atomicAdd(&hist[q.z >> 20], 1);
+              if (q.w) atomicAdd(&hist[q.w >> 20], 1);
+            }
           }
-        }
-      } else {
-        const unsigned above = thr >> (sh + 10);
-#pragma unroll 4
-        for (int j = 0; j < live; ++j) {
-          const unsigned u = get(j);
-          if (u != 0u && (u >> (sh + 10)) == above) atomicAdd(&hist[(u >> sh) & 1023u], 1);
+        } else {
+          // no key is 0 above the digits: bit patterns of "no token" never match
+          const unsigned above = thr >> (sh + 10);
+          for (int c = 0; c < cpl; ++c) {
+            const uint4 q = my_keys[c];
+            if ((q.x >> (sh + 10)) == above) atomicAdd(&hist[(q.x >> sh) & 1023u], 1);
+            if ((q.y >> (sh + 10)) == above) atomicAdd(&hist[(q.y >> sh) & 1023u], 1);
+            if ((q.z >> (sh + 10)) == above) atomicAdd(&hist[(q.z >> sh) & 1023u], 1);
+            if ((q.w >> (sh + 10)) == above) atomicAdd(&hist[(q.w >> sh) & 1023u], 1);
+          }
         }
       }
       __syncthreads();
@@ -213,13 +310,16 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs) {
       const int* gs = cs > 1 ? s_gsum : s_group[pass];
       int c[4] = {0, 0, 0, 0}, group = 0, before = 0;
       const int per = groups / 32, top = groups - 1 - per * lane;  // this lane's first group
-      for (int q = 0; q < per; ++q) c[q] = gs[top - q];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) c[q] = q < per ? gs[top - q] : 0;
       const int mine = (c[0] + c[1]) + (c[2] + c[3]), upto = warp_inclusive(mine, lane);
       {
         const unsigned hit = __ballot_sync(0xffffffffu, upto >= want);  // not empty: want of them exist
         const int l = __ffs(hit) - 1;
         int q = 0, at = upto - mine;
-        while (q < per - 1 && at + c[q] < want) at += c[q++];
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (q == e && e < per - 1 && at + c[e] < want) { at += c[e]; ++q; }
         group = __shfl_sync(0xffffffffu, top - q, l);
         before = __shfl_sync(0xffffffffu, at, l);
       }
@@ -236,73 +336,74 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs) {
       const int v = cs > 1 ? s_bsum[31 - lane] : hist[group * 32 + 31 - lane];
       const int sum = before + warp_inclusive(v, lane);
       const int l = __ffs(__ballot_sync(0xffffffffu, sum >= want)) - 1;
+      const int in_bin = __shfl_sync(0xffffffffu, v, l);
       thr |= (unsigned)(group * 32 + 31 - l) << sh;
-      const int upper = __shfl_sync(0xffffffffu, sum, l);
-      want -= upper - __shfl_sync(0xffffffffu, v, l);
-      whole = want == __shfl_sync(0xffffffffu, v, l);
+      want -= __shfl_sync(0xffffffffu, sum, l) - in_bin;
+      whole = want == in_bin;
     }
 
     // ---- keep words; equal keys beyond `want` leave from the highest index down
-    int tie_left = 0;                    // equal keys that may stay, from this warp on
-    if (!whole) {
-      int ties = 0;
-      for (int j = 0; j < live; ++j) ties += __popc(__ballot_sync(0xffffffffu, get(j) == thr));
-      if (lane == 0) s_wt[0][warp] = ties;
-      __syncthreads();
-      const int t = s_wt[0][lane];
-      int before = __reduce_add_sync(0xffffffffu, lane < warp ? t : 0);
-      if (cs > 1) {
-        const int all = __reduce_add_sync(0xffffffffu, t);
-        if (tid == 0) s_ct[1] = all;
-        cluster_sync();
-        before += __reduce_add_sync(0xffffffffu, lane < rank ? peer_int(&s_ct[1], lane) : 0);
-      }
-      tie_left = max(0, want - before);
-    }
-    // this lane's word of iterations j0 .. j0 + 31: bit i = token w0 + 32 (j0 + lane) + i
-    int tie_run = tie_left;
-    auto keep_word = [&](int j0) {
-      const int nj = min(32, live - j0);
-      unsigned w = 0u, tw = 0u;
-#pragma unroll 4
-      for (int j = 0; j < nj; ++j) {
-        const unsigned u = get(j0 + j);
-        const unsigned kw = __ballot_sync(0xffffffffu, whole ? u >= thr : u > thr);
-        if (lane == j) w = kw;
-        if (!whole) {
-          const unsigned e = __ballot_sync(0xffffffffu, u == thr);
-          if (lane == j) tw = e;
-        }
-      }
-      if (!whole) {
-        const int c = __popc(tw), upto = warp_inclusive(c, lane);
-        const int stay = min(c, max(0, tie_run - (upto - c)));
-        tie_run = max(0, tie_run - __shfl_sync(0xffffffffu, upto, 31));
-        for (int drop = c - stay; drop > 0; --drop) tw &= ~(0x80000000u >> __clz(tw));
-        w |= tw;
+    auto word_of = [&](auto in) {        // bit i: in(key of this lane's token i)
+      unsigned long long w = 0ull;
+      for (int c = 0; c < cpl; ++c) {
+        const uint4 q = my_keys[c];
+        const unsigned f = (in(q.x) ? 1u : 0u) | (in(q.y) ? 2u : 0u) | (in(q.z) ? 4u : 0u) | (in(q.w) ? 8u : 0u);
+        w |= (unsigned long long)f << (4 * c);
       }
       return w;
     };
-    // this lane's tokens before the budget, as a mask
-    auto front_word = [&](int j0) {
-      const long long m = j0 + lane < live ? a.budget - (w0 + 32 * (j0 + lane)) : 0;
-      return m <= 0 ? 0u : m >= 32 ? 0xffffffffu : (1u << (int)m) - 1u;
+    const unsigned thr_c = thr;
+    int tie_first = 0;                   // equal keys of the CTAs before this one
+    if (!whole && cs > 1) {
+      int ties = 0;
+      for (int k = 0; k < tiles; ++k) {
+        if (tiles > 1) load_tile(k);
+        ties += __popcll(word_of([&](unsigned u) { return u == thr_c; }));
+      }
+      ties = __reduce_add_sync(0xffffffffu, ties);
+      if (lane == 0) s_wt[0][warp] = ties;
+      __syncthreads();
+      const int all = __reduce_add_sync(0xffffffffu, s_wt[0][lane]);
+      if (tid == 0) s_ct[1] = all;
+      cluster_sync();
+      tie_first = __reduce_add_sync(0xffffffffu, lane < rank ? peer_int(&s_ct[1], lane) : 0);
+    }
+    // this lane's keep bits of tile k; `seen`: equal keys of the tiles before
+    auto keep_word = [&](int k, int& seen) {
+      if (tiles > 1) load_tile(k);
+      if (whole) return word_of([&](unsigned u) { return u >= thr_c; });
+      unsigned long long tw = word_of([&](unsigned u) { return u == thr_c; });
+      const int c = __popcll(tw), upto = warp_inclusive(c, lane);
+      __syncthreads();                   // the last counts are no longer read
+      if (lane == 31) s_wt[0][warp] = upto;
+      __syncthreads();
+      const int t = s_wt[0][lane];
+      const int before = seen + __reduce_add_sync(0xffffffffu, lane < warp ? t : 0) + upto - c;
+      seen += __reduce_add_sync(0xffffffffu, t);
+      const int stay = min(c, max(0, want - before));
+      for (int drop = c - stay; drop > 0; --drop) tw &= ~(0x8000000000000000ull >> __clzll(tw));
+      return tw | word_of([&](unsigned u) { return u > thr_c; });
     };
-    unsigned word = 0u;
-    int holes = 0, fills = 0;
-    for (int j0 = 0; j0 < live; j0 += 32) {
-      word = keep_word(j0);
-      const unsigned front = front_word(j0);
-      holes += __popc(~word & front);    // budget < n: every token before it exists
-      fills += __popc(word & ~front);
+    auto lane_at = [&](int k) { return warp_at(k) + (long long)lane * it; };
+    // this lane's tokens before the budget (they exist: budget < n), as a mask
+    auto front_word = [&](int k) {
+      const long long m = a.budget - lane_at(k);
+      return m <= 0 ? 0ull : (1ull << (int)min(m, (long long)it)) - 1ull;  // it <= 44
+    };
+    unsigned long long word = 0ull;
+    int holes = 0, fills = 0, seen = tie_first;
+    for (int k = 0; k < tiles; ++k) {
+      word = keep_word(k, seen);
+      const unsigned long long front = front_word(k);
+      holes += __popcll(~word & front);
+      fills += __popcll(word & ~front);
     }
     holes = __reduce_add_sync(0xffffffffu, holes);
     fills = __reduce_add_sync(0xffffffffu, fills);
     if (lane == 0) { s_wt[1][warp] = holes; s_wt[2][warp] = fills; }
     __syncthreads();
     const int th = s_wt[1][lane], tf = s_wt[2][lane];
-    int hole_at = __reduce_add_sync(0xffffffffu, lane < warp ? th : 0);
-    int fill_at = __reduce_add_sync(0xffffffffu, lane < warp ? tf : 0);
+    int hole_first = 0, fill_first = 0;  // of the CTAs before this one
     moves = __reduce_add_sync(0xffffffffu, tf);
     if (cs > 1) {
       const int all_h = __reduce_add_sync(0xffffffffu, th);
@@ -311,35 +412,33 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs) {
       const int f = lane < cs ? peer_int(&s_ct[3], lane) : 0;
       const int h = lane < rank ? peer_int(&s_ct[2], lane) : 0;
       moves = __reduce_add_sync(0xffffffffu, f);
-      hole_at += __reduce_add_sync(0xffffffffu, h);
-      fill_at += __reduce_add_sync(0xffffffffu, lane < rank ? f : 0);
+      hole_first = __reduce_add_sync(0xffffffffu, h);
+      fill_first = __reduce_add_sync(0xffffffffu, lane < rank ? f : 0);
     }
-    tie_run = tie_left;
-    // Lists the set bits of the lanes' words in order, from list[at] on: word
-    // by word, so that neighbours are written together, or each lane its own
-    // when no word is crowded.
-    auto list = [&](unsigned w, int32_t* out, int at, int j0) {
-      const int c = __popc(w), upto = warp_inclusive(c, lane);
-      if (__reduce_max_sync(0xffffffffu, c) <= 12) {
-        int32_t* o = out + at + upto - c;
-        const int t0 = (int)(w0 + 32 * (j0 + lane));
-        for (; w; w &= w - 1) *o++ = t0 + __ffs(w) - 1;
-      } else {
-        const unsigned bit = 1u << lane;
-        for (unsigned some = __ballot_sync(0xffffffffu, w != 0u); some; some &= some - 1) {
-          const int j = __ffs(some) - 1;
-          const unsigned v = __shfl_sync(0xffffffffu, w, j);
-          const int o = at + __shfl_sync(0xffffffffu, upto - c, j);
-          if (v & bit) out[o + __popc(v & (bit - 1))] = (int)(w0 + 32 * (j0 + j)) + lane;
-        }
+    if (tiles == 1) {
+      const unsigned long long front = front_word(0);
+      list_bits(~word & front, hole, hole_first + __reduce_add_sync(0xffffffffu, lane < warp ? th : 0),
+                lane_at(0), it, lane);
+      list_bits(word & ~front, fill, fill_first + __reduce_add_sync(0xffffffffu, lane < warp ? tf : 0),
+                lane_at(0), it, lane);
+    } else {
+      seen = tie_first;
+      for (int k = 0; k < tiles; ++k) {
+        word = keep_word(k, seen);
+        const unsigned long long front = front_word(k);
+        const int h = __reduce_add_sync(0xffffffffu, __popcll(~word & front));
+        const int f = __reduce_add_sync(0xffffffffu, __popcll(word & ~front));
+        __syncthreads();
+        if (lane == 0) { s_wt[1][warp] = h; s_wt[2][warp] = f; }
+        __syncthreads();
+        const int uh = s_wt[1][lane], uf = s_wt[2][lane];
+        list_bits(~word & front, hole, hole_first + __reduce_add_sync(0xffffffffu, lane < warp ? uh : 0),
+                  lane_at(k), it, lane);
+        list_bits(word & ~front, fill, fill_first + __reduce_add_sync(0xffffffffu, lane < warp ? uf : 0),
+                  lane_at(k), it, lane);
+        hole_first += __reduce_add_sync(0xffffffffu, uh);
+        fill_first += __reduce_add_sync(0xffffffffu, uf);
       }
-      return at + __shfl_sync(0xffffffffu, upto, 31);
-    };
-    for (int j0 = 0; j0 < live; j0 += 32) {
-      if (live > 32) word = keep_word(j0);
-      const unsigned front = front_word(j0);
-      hole_at = list(~word & front, hole, hole_at, j0);
-      fill_at = list(word & ~front, fill, fill_at, j0);
     }
     if (cs > 1) cluster_sync();          // no CTA leaves while its counts are read
   }
@@ -419,16 +518,14 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, int groups, long lon
   }
 }
 
-template <bool KEEP>
-cudaError_t run_evict(const EvictArgs& a, int cs, size_t smem, cudaStream_t st) {
-  auto kern = evict_select_kernel<KEEP>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kKeepTokens * kEvThreads * 4);
+template <bool VEC>
+cudaError_t run_evict(const EvictArgs& a, int cs, int it, cudaStream_t st) {
+  cudaError_t e = allow_smem<evict_select_kernel<VEC>>((kMaxIt / 4 | 1) * 16 * kEvThreads);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.s.batch * a.n_mass) * cs);
   cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = (size_t)(it / 4 | 1) * 16 * kEvThreads;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -438,7 +535,7 @@ cudaError_t run_evict(const EvictArgs& a, int cs, size_t smem, cudaStream_t st) 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, cs);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<VEC>, a, cs, it);
 }
 
 }  // namespace
@@ -450,11 +547,13 @@ cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st) {
   const int sms = tc_sm_count();
   int cs = 1;
   while (cs < kMaxCluster && ((rows * cs * 2 <= sms && L > (long long)cs * kEvThreads) ||
-                              L > (long long)cs * kKeepTokens * kEvThreads))
+                              L > (long long)cs * kMaxIt * kEvThreads))
     cs *= 2;
-  const long long it = (L + (long long)cs * kEvThreads - 1) / ((long long)cs * kEvThreads);
-  if (it <= kKeepTokens) return run_evict<true>(a, cs, (size_t)it * kEvThreads * 4, st);
-  return run_evict<false>(a, cs, 0, st);
+  const long long per = (L + 4ll * cs * kEvThreads - 1) / (4ll * cs * kEvThreads) * 4;
+  const int it = (int)(per < kMaxIt ? (per > 0 ? per : 4) : kMaxIt);
+  const bool vec = L % 4 == 0 && (reinterpret_cast<uintptr_t>(a.tok_mass) & 15) == 0 &&
+                   (reinterpret_cast<uintptr_t>(a.tok_pos) & 15) == 0;
+  return vec ? run_evict<true>(a, cs, it, st) : run_evict<false>(a, cs, it, st);
 }
 
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {
