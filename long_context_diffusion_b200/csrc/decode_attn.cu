@@ -95,9 +95,16 @@ __device__ __forceinline__ int seq_len(const DecodeArgs& a, int b) {
   return n >= 0 && n <= a.s.L_ctx ? n : 0;
 }
 
+// a b / c and the like on tile counts: 32 bits where they suffice (a 64-bit
+// division is a long chain at the head of every CTA).
+__device__ __forceinline__ long long div_tiles(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (unsigned)x / (unsigned)y;
+  return x / y;
+}
+
 // CTA that owns tile u when T tiles are cut into P runs [c T / P, (c + 1) T / P).
 __device__ __forceinline__ int run_of(long long u, long long T, int P) {
-  return (int)(((u + 1) * P - 1) / T);
+  return (int)div_tiles((u + 1) * P - 1, T);
 }
 
 // One run's part of an item.
@@ -110,13 +117,12 @@ struct Walk {
   const DecodeArgs& a;
   long long left;  // tiles of the run still to walk
   int ips, kt, b, item, t, nt, len;
-  __device__ Walk(const DecodeArgs& a_, int ips_, int kt_, int b_, long long off, long long n)
-      : a(a_), left(n), ips(ips_), kt(kt_), b(b_) {
-    if (left <= 0) return;
-    len = seq_len(a, b);
+  // The run [lo, lo + n) starts `off` tiles into sequence b_ of len_ tokens.
+  __device__ Walk(const DecodeArgs& a_, int ips_, int kt_, int b_, int len_, long long off, long long n)
+      : a(a_), left(n), ips(ips_), kt(kt_), b(b_), len(len_) {
     nt = (len + kt - 1) / kt;
-    item = (int)(off / nt);
-    t = (int)(off % nt);
+    item = (int)div_tiles(off, nt);
+    t = (int)(off - (long long)item * nt);
   }
   __device__ bool next(Segment* s) {
     if (left <= 0) return false;
@@ -515,8 +521,6 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
   uint64_t* empty = full + C::ST;
   volatile int* info = reinterpret_cast<volatile int*>(sm + C::MISC_OFF);
   volatile int* abort_flag = info + C::ST;
-  __shared__ long long s_scan[kThreads / 32], s_off;
-  __shared__ int s_b;
   __shared__ float s_f[kWarps][RB];
   const Shape& s = a.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -527,20 +531,23 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     *abort_flag = 0;
   }
   if (warp == kWarps && lane == 0) { prefetch_tmap(&mk); prefetch_tmap(&mv); }
+  pdl_trigger();
   pdl_wait();
 
-  // This CTA's run: tiles [lo, hi) of the total of all sequences.  Each thread
-  // counts a run of sequences; the one whose count reaches lo finds the place.
-  const int per = (s.batch + kThreads - 1) / kThreads, b0 = min(s.batch, tid * per),
-            b1 = min(s.batch, b0 + per);
+  // This CTA's run: tiles [lo, hi) of the total of all sequences.  Every warp
+  // finds it for itself: a lane counts `per` sequences; the one whose count
+  // passes lo has the place.
+  const int per = (s.batch + 31) / 32, b0 = min(s.batch, lane * per), b1 = min(s.batch, b0 + per);
   long long mine = 0;
+  int n0 = 0;                            // length of sequence b0
+#pragma unroll 4
   for (int b = b0; b < b1; ++b) {
     const int n = a.ctx_len[b];
-    if (n < 0 || n > s.L_ctx) {
-      if (blockIdx.x == 0) flag_error(a.err, ERR_BAD_INDEX);
-    } else {
-      mine += (long long)((n + C::KT - 1) / C::KT) * ips;
-    }
+    const bool ok = n >= 0 && n <= s.L_ctx;
+    if (!ok && blockIdx.x == 0 && warp == 0) flag_error(a.err, ERR_BAD_INDEX);
+    const int len = ok ? n : 0;
+    if (b == b0) n0 = len;
+    mine += (long long)((len + C::KT - 1) / C::KT) * ips;
   }
   long long before = mine;
 #pragma unroll
@@ -548,37 +555,38 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     const long long v = __shfl_up_sync(0xffffffffu, before, o);
     if (lane >= o) before += v;
   }
-  if (lane == 31) s_scan[warp] = before;
+  const long long total = __shfl_sync(0xffffffffu, before, 31);
   before -= mine;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
-  }
   const int P = (int)min((long long)gridDim.x, total);  // runs that hold a tile
   const int c = blockIdx.x;
-  if (c == 0) {  // for the join kernel
+  if (c == 0 && warp == 0) {  // for the join kernel
     long long at = before;
     for (int b = b0; b < b1; ++b) {
       ws.first[b] = at;
       at += (long long)((seq_len(a, b) + C::KT - 1) / C::KT) * ips;
     }
-    if (tid == 0) ws.first[s.batch] = total;
+    if (lane == 0) ws.first[s.batch] = total;
   }
   if (c >= P) return;
-  const long long lo = total * c / P, hi = total * (c + 1) / P;
-  if (lo >= before && lo < before + mine) {
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      const long long w = (long long)((seq_len(a, b) + C::KT - 1) / C::KT) * ips;
-      if (lo < at + w) { s_b = b; s_off = lo - at; break; }
+  const long long lo = div_tiles(total * c, P), hi = div_tiles(total * (c + 1), P);
+  int wb = b0, wlen = n0;
+  long long woff = lo - before;
+  const bool here = lo >= before && lo < before + mine;
+  if (here && per > 1) {
+    for (long long at = before; wb < b1; ++wb) {
+      wlen = seq_len(a, wb);
+      const long long w = (long long)((wlen + C::KT - 1) / C::KT) * ips;
+      woff = lo - at;
+      if (woff < w) break;
       at += w;
     }
   }
-  __syncthreads();
-  Walk walk(a, ips, C::KT, s_b, s_off, hi - lo);
+  const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  wb = __shfl_sync(0xffffffffu, wb, src);
+  wlen = __shfl_sync(0xffffffffu, wlen, src);
+  woff = __shfl_sync(0xffffffffu, woff, src);
+  __syncthreads();                       // the barriers are set up
+  Walk walk(a, ips, C::KT, wb, wlen, woff, hi - lo);
   Segment seg;
 
   if (warp == kWarps) {
@@ -749,6 +757,28 @@ __device__ __forceinline__ Parts parts_of(const DecodeArgs& a, const DecodeWs& w
   return p;
 }
 
+// Base-2 log-sum of one query row over its runs, by one warp.  A row finished
+// by its run has it in the workspace.
+__device__ __forceinline__ float row_lse2(const DecodeArgs& a, const DecodeWs& ws, const Parts& p, size_t row,
+                                          int rb, int lane) {
+  if (p.n == 1) return ws.lse2[row];
+  constexpr int N = (kMaxCtas + 31) / 32;
+  float2 v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    v[i] = lane + 32 * i < p.n ? ws.pml[(size_t)p.slot(lane + 32 * i) * rb + p.r]
+                               : make_float2(-INFINITY, 0.0f);
+  float M = -INFINITY, L = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) M = fmaxf(M, v[i].x);
+  M = warp_max(M);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (v[i].x != -INFINITY) L = fmaf(v[i].y, ex2_approx(v[i].x - M), L);
+  L = warp_sum(L);
+  return M + log2f(L);
+}
+
 // CTAs [0, batch * H): join the partials of one query row (or write an empty
 // sequence's row).  The others: masses of kMassChunk tokens at a time.
 template <typename T, int D>
@@ -759,56 +789,82 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
   const Shape& s = a.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (blockIdx.x < s.batch * s.H) {
-    __shared__ float s_m[8], s_l[8];
+    __shared__ float s_m[8], s_l[8], s_w[kMaxCtas];
     __shared__ float4 s_o[256];
     const int row = blockIdx.x, b = row / s.H;
     const Parts p = parts_of(a, ws, P0, b, row % s.H, rb, kt);
     if (p.n == 1) return;  // finished by its run
-    // maximum and sum over the runs
+    // a thread's outputs are under way while the weights are found: thread =
+    // (part group, four columns)
+    constexpr int CH = D / 4, GR = 256 / CH, U = 10;
+    const int col = tid % CH, grp = tid / CH;
+    const float4* po = reinterpret_cast<const float4*>(ws.po) + (size_t)p.r * CH + col;
+    const size_t step = (size_t)rb * CH;
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = grp + u * GR;
+      v[u] = i < p.n ? po[p.slot(i) * step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    constexpr int N = (kMaxCtas + 255) / 256;
+    float2 ml[N];
     float M = -INFINITY, L = 0.0f;
-    for (int i = tid; i < p.n; i += 256) M = fmaxf(M, ws.pml[(size_t)p.slot(i) * rb + p.r].x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      ml[i] = tid + 256 * i < p.n ? ws.pml[(size_t)p.slot(tid + 256 * i) * rb + p.r]
+                                  : make_float2(-INFINITY, 0.0f);
+      M = fmaxf(M, ml[i].x);
+    }
     M = warp_max(M);
     if (lane == 0) s_m[warp] = M;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < 8; ++w) M = fmaxf(M, s_m[w]);
-    for (int i = tid; i < p.n; i += 256) {
-      const float2 v = ws.pml[(size_t)p.slot(i) * rb + p.r];
-      if (v.x != -INFINITY) L = fmaf(v.y, ex2_approx(v.x - M), L);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float f = ml[i].x == -INFINITY ? 0.0f : ex2_approx(ml[i].x - M);
+      if (tid + 256 * i < p.n) s_w[tid + 256 * i] = f;
+      L = fmaf(ml[i].y, f, L);
     }
     L = warp_sum(L);
     if (lane == 0) s_l[warp] = L;
-    // outputs: thread = (part group, four columns)
-    constexpr int CH = D / 4, GR = 256 / CH;
-    const int col = tid % CH, grp = tid / CH;
+    __syncthreads();
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = grp; i < p.n; i += GR) {
-      const size_t at = (size_t)p.slot(i) * rb + p.r;
-      const float m = ws.pml[at].x;
-      const float4 v = reinterpret_cast<const float4*>(ws.po)[at * CH + col];
-      const float f = m == -INFINITY ? 0.0f : ex2_approx(m - M);
-      o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+    for (int i0 = grp; i0 < p.n; i0 += U * GR) {
+      if (i0 != grp) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * GR;
+          v[u] = i < p.n ? po[p.slot(i) * step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * GR;
+        const float f = i < p.n ? s_w[i] : 0.0f;
+        o.x = fmaf(f, v[u].x, o.x); o.y = fmaf(f, v[u].y, o.y);
+        o.z = fmaf(f, v[u].z, o.z); o.w = fmaf(f, v[u].w, o.w);
+      }
     }
     s_o[tid] = o;
     __syncthreads();
-    L = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) L += s_l[w];
     if (tid < CH) {
+      L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) L += s_l[w];
+#pragma unroll
       for (int i = 1; i < GR; ++i) {
-        const float4 v = s_o[i * CH + tid];
-        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+        const float4 x = s_o[i * CH + tid];
+        o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
       }
       float inv = L > 0.0f ? 1.0f / L : 0.0f;
       if (L != L) inv = L;
       T* dst = reinterpret_cast<T*>(a.O) + (size_t)row * D + 4 * tid;
       store2(dst, make_float2(o.x * inv, o.y * inv));
       store2(dst + 2, make_float2(o.z * inv, o.w * inv));
+      if (tid == 0 && a.lse)
+        a.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : (L != L ? L : -INFINITY);
     }
-    if (tid == 0 && a.lse)
-      a.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : (L != L ? L : -INFINITY);
     return;
   }
   // ---- masses
@@ -816,33 +872,22 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
   const int id = blockIdx.x - s.batch * s.H;
   const int bm = id / chunks, b = bm / a.n_mass, m = bm % a.n_mass;
   const int n = seq_len(a, b), rows = s.H / a.n_mass, h0 = m * rows;
+  constexpr int TU = kMassChunk / 256;
   for (int t0 = (id % chunks) * kMassChunk; t0 < n; t0 += chunks * kMassChunk) {
-    float sum[kMassChunk / 256];
+    float sum[TU], old[TU];
+    float* dst = a.tok_mass + ((size_t)b * a.n_mass + m) * s.L_ctx + t0 + tid;
 #pragma unroll
-    for (int j = 0; j < kMassChunk / 256; ++j) sum[j] = 0.0f;
+    for (int j = 0; j < TU; ++j) {
+      sum[j] = 0.0f;
+      old[j] = a.decay != 0.0f && t0 + tid + 256 * j < n ? dst[256 * j] : 0.0f;
+    }
     for (int r0 = 0; r0 < rows; r0 += 32) {
-      // the rows' sums, eight lanes a row
       __syncthreads();
-      const int r = r0 + tid / 8, ln = tid % 8;
-      float M = -INFINITY, L = 0.0f, lse = INFINITY;
-      if (r < rows) {
-        const Parts p = parts_of(a, ws, P0, b, h0 + r, rb, kt);
-        if (p.n == 1) {
-          lse = ws.lse2[(size_t)b * s.H + h0 + r];
-        } else {
-          for (int i = ln; i < p.n; i += 8) M = fmaxf(M, ws.pml[(size_t)p.slot(i) * rb + p.r].x);
-#pragma unroll
-          for (int w = 1; w < 8; w <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffu << (lane & 24), M, w));
-          for (int i = ln; i < p.n; i += 8) {
-            const float2 v = ws.pml[(size_t)p.slot(i) * rb + p.r];
-            if (v.x != -INFINITY) L = fmaf(v.y, ex2_approx(v.x - M), L);
-          }
-#pragma unroll
-          for (int w = 1; w < 8; w <<= 1) L += __shfl_xor_sync(0xffu << (lane & 24), L, w);
-          lse = M + log2f(L);
-        }
+      for (int r = r0 + warp; r < min(rows, r0 + 32); r += 8) {
+        const float lse = row_lse2(a, ws, parts_of(a, ws, P0, b, h0 + r, rb, kt),
+                                   (size_t)b * s.H + h0 + r, rb, lane);
+        if (lane == 0) s_lse[r - r0] = lse == -INFINITY ? INFINITY : lse;  // no weight at all: 2^-inf
       }
-      if (ln == 0) s_lse[tid / 8] = lse == -INFINITY ? INFINITY : lse;  // no weight at all: 2^-inf
       __syncthreads();
       const int nr = min(32, rows - r0);
       const float* x = ws.logit + ((size_t)b * s.H + h0 + r0) * ws.Lp + t0 + tid;
@@ -850,16 +895,13 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
       for (int q = 0; q < nr; ++q) {
         const float l2 = s_lse[q];
 #pragma unroll
-        for (int j = 0; j < kMassChunk / 256; ++j)
+        for (int j = 0; j < TU; ++j)
           if (t0 + tid + 256 * j < n) sum[j] += ex2_approx(x[(size_t)q * ws.Lp + 256 * j] - l2);
       }
     }
-    float* dst = a.tok_mass + ((size_t)b * a.n_mass + m) * s.L_ctx + t0 + tid;
 #pragma unroll
-    for (int j = 0; j < kMassChunk / 256; ++j) {
-      if (t0 + tid + 256 * j < n)
-        dst[256 * j] = a.decay == 0.0f ? sum[j] : fmaf(a.decay, dst[256 * j], sum[j]);
-    }
+    for (int j = 0; j < TU; ++j)
+      if (t0 + tid + 256 * j < n) dst[256 * j] = a.decay == 0.0f ? sum[j] : fmaf(a.decay, old[j], sum[j]);
   }
 }
 
@@ -889,7 +931,7 @@ cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
     chunks = chunks < 4096 ? chunks : 4096;
   }
   auto join = decode_join_kernel<T, D>;
-  DL_LAUNCH(join, s.batch * s.H + s.batch * a.n_mass * chunks, 256, 0, st, a, w, P, RB, C::KT,
+  DL_LAUNCH_DEPENDENT(join, s.batch * s.H + s.batch * a.n_mass * chunks, 256, 0, st, a, w, P, RB, C::KT,
             chunks > 0 ? chunks : 1);
   return cudaGetLastError();
 }

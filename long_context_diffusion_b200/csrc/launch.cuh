@@ -36,9 +36,11 @@ __device__ __forceinline__ void pdl_trigger() {
 
 inline bool pdl_enabled() { return (kernel_flags() & DL_FLAG_PDL) != 0; }
 
+// `dependent`: programmatic even without the flag, for the second kernel of one
+// call, whose launch and prologue then overlap the first.
 template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                   Args&&... args) {
+cudaError_t launch_as(bool dependent, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                      cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -48,8 +50,14 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  cfg.numAttrs = dependent || pdl_enabled() ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                   Args&&... args) {
+  return launch_as(false, kernel, grid, block, smem, st, std::forward<Args>(args)...);
 }
 
 // Allows `bytes` of dynamic shared memory to a kernel, once per device.
@@ -69,6 +77,11 @@ cudaError_t allow_smem(int bytes) {
 }  // namespace dl
 
 // Launches and returns the launch error from the enclosing function.
+#define DL_LAUNCH_DEPENDENT(...)                              \
+  do {                                                        \
+    cudaError_t dl_le_ = ::dl::launch_as(true, __VA_ARGS__);  \
+    if (dl_le_ != cudaSuccess) return dl_le_;                 \
+  } while (0)
 #define DL_LAUNCH(...)                                   \
   do {                                                   \
     cudaError_t dl_le_ = ::dl::launch(__VA_ARGS__);      \
