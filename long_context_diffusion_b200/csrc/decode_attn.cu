@@ -10,7 +10,8 @@
 // keys are tiles of KT.  The tiles of all items, in order, are cut into one
 // equal run per CTA, whatever the lengths are: the lengths are read on the
 // device, so a batch of very different sequences stays balanced and a single
-// long one spreads over the whole GPU.  A run is walked item by item
+// long one spreads over the whole GPU.  An item counts as kItemCost tiles more
+// than it has, for what its start and end take.  A run is walked item by item
 // (segments).  An item inside one run is finished there; otherwise each of
 // its runs leaves a partial (maximum, sum, unnormalised output) in the
 // workspace, and the join kernel adds them in run order.
@@ -52,7 +53,7 @@ constexpr int kWarps = 4;                       // computing warps
 constexpr int kThreads = (kWarps + 1) * 32;     // + the copying warp
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 148 * kCtasPerSm;      // partial slots are sized for this many
-constexpr int kMassChunk = 1024;                // tokens of one mass CTA
+constexpr int kJoinThreads = 256;
 constexpr float kLn2 = 0.69314718055994531f;
 
 // Query heads per item block: 8, or 16 for bf16 groups of more than 8.
@@ -64,8 +65,13 @@ __host__ __device__ inline int items_per_seq(const Shape& s) {
   return s.H_kv * ((s.G + rb - 1) / rb);
 }
 
+// Extra count of an item: at full load a tile takes 1.5 us of a CTA, an item's
+// query load, state join and output 3 to 4 us (ragged 32 x 8K: 0 -> 78 us, 1 ->
+// 70, 3 -> 68, 8 -> 69).
+constexpr int kItemCost = 3;
+
 struct DecodeWs {
-  long long* first;  // [batch + 1]: tiles before each sequence, then all
+  int* runs;         // [batch][items][2]: first and last run of each item
   float* po;         // [2 kMaxCtas][RB][d] unnormalised partial outputs
   float2* pml;       // [2 kMaxCtas][RB] (maximum, sum), base-2 units
   float* lse2;       // [batch][H] of the items finished in one run, base-2
@@ -80,7 +86,7 @@ size_t carve(const Shape& s, bool mass, void* ws, DecodeWs* w) {
   auto take = [&](size_t n) { char* q = p + at; at += round256(n); return q; };
   DecodeWs d;
   d.Lp = (s.L_ctx + 63) / 64 * 64;
-  d.first = reinterpret_cast<long long*>(take((size_t)(s.batch + 1) * 8));
+  d.runs = reinterpret_cast<int*>(take((size_t)s.batch * items_per_seq(s) * 8));
   d.po = reinterpret_cast<float*>(take((size_t)2 * kMaxCtas * rb * s.d * 4));
   d.pml = reinterpret_cast<float2*>(take((size_t)2 * kMaxCtas * rb * 8));
   d.lse2 = reinterpret_cast<float*>(take((size_t)s.batch * s.H * 4));
@@ -102,40 +108,42 @@ __device__ __forceinline__ long long div_tiles(long long x, long long y) {
   return x / y;
 }
 
-// CTA that owns tile u when T tiles are cut into P runs [c T / P, (c + 1) T / P).
-__device__ __forceinline__ int run_of(long long u, long long T, int P) {
-  return (int)div_tiles((u + 1) * P - 1, T);
-}
-
 // One run's part of an item.
 struct Segment {
   int b, item, t0, t1, nt, len;
 };
 
+// Tiles that a sequence of `len` tokens counts as.
+__device__ __forceinline__ long long seq_cost(int len, int kt, int ips) {
+  return len == 0 ? 0 : (long long)((len + kt - 1) / kt + kItemCost) * ips;
+}
+
 // Walks the segments of a run; every role of a CTA walks the same ones.
 struct Walk {
   const DecodeArgs& a;
-  long long left;  // tiles of the run still to walk
-  int ips, kt, b, item, t, nt, len;
-  // The run [lo, lo + n) starts `off` tiles into sequence b_ of len_ tokens.
+  long long left;  // of the run, in counted tiles
+  int ips, kt, b, item, v, nt, len;
+  // The run of n counted tiles starts `off` of them into sequence b_ of len_ tokens.
   __device__ Walk(const DecodeArgs& a_, int ips_, int kt_, int b_, int len_, long long off, long long n)
       : a(a_), left(n), ips(ips_), kt(kt_), b(b_), len(len_) {
     nt = (len + kt - 1) / kt;
-    item = (int)div_tiles(off, nt);
-    t = (int)(off - (long long)item * nt);
+    item = (int)div_tiles(off, nt + kItemCost);
+    v = (int)(off - (long long)item * (nt + kItemCost));
   }
   __device__ bool next(Segment* s) {
-    if (left <= 0) return false;
-    const int n = (int)min((long long)(nt - t), left);
-    *s = Segment{b, item, t, t + n, nt, len};
-    left -= n;
-    t = 0;
-    if (left > 0 && ++item == ips) {
-      item = 0;
-      do len = seq_len(a, ++b); while (len == 0);
-      nt = (len + kt - 1) / kt;
+    while (left > 0) {
+      const int n = (int)min((long long)(nt + kItemCost - v), left);
+      *s = Segment{b, item, max(0, v - kItemCost), max(0, v + n - kItemCost), nt, len};
+      left -= n;
+      v = 0;
+      if (left > 0 && ++item == ips) {
+        item = 0;
+        do len = seq_len(a, ++b); while (len == 0);
+        nt = (len + kt - 1) / kt;
+      }
+      if (s->t1 > s->t0) return true;  // else the run ends inside the item's extra count
     }
-    return true;
+    return false;
   }
 };
 
@@ -531,8 +539,8 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     *abort_flag = 0;
   }
   if (warp == kWarps && lane == 0) { prefetch_tmap(&mk); prefetch_tmap(&mv); }
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();                         // after the wait: the join kernel reads the lengths before its own
 
   // This CTA's run: tiles [lo, hi) of the total of all sequences.  Every warp
   // finds it for itself: a lane counts `per` sequences; the one whose count
@@ -547,7 +555,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     if (!ok && blockIdx.x == 0 && warp == 0) flag_error(a.err, ERR_BAD_INDEX);
     const int len = ok ? n : 0;
     if (b == b0) n0 = len;
-    mine += (long long)((len + C::KT - 1) / C::KT) * ips;
+    mine += seq_cost(len, C::KT, ips);
   }
   long long before = mine;
 #pragma unroll
@@ -559,14 +567,6 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
   before -= mine;
   const int P = (int)min((long long)gridDim.x, total);  // runs that hold a tile
   const int c = blockIdx.x;
-  if (c == 0 && warp == 0) {  // for the join kernel
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      ws.first[b] = at;
-      at += (long long)((seq_len(a, b) + C::KT - 1) / C::KT) * ips;
-    }
-    if (lane == 0) ws.first[s.batch] = total;
-  }
   if (c >= P) return;
   const long long lo = div_tiles(total * c, P), hi = div_tiles(total * (c + 1), P);
   int wb = b0, wlen = n0;
@@ -575,7 +575,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
   if (here && per > 1) {
     for (long long at = before; wb < b1; ++wb) {
       wlen = seq_len(a, wb);
-      const long long w = (long long)((wlen + C::KT - 1) / C::KT) * ips;
+      const long long w = seq_cost(wlen, C::KT, ips);
       woff = lo - at;
       if (woff < w) break;
       at += w;
@@ -710,6 +710,11 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
       if (w0 + C::COPIES < kWarps) named_bar_sync(1, kWarps * 32);
     }
     if (warp != 0) continue;
+    if (lane == 0) {                     // for the join kernel
+      int* runs = ws.runs + ((size_t)seg.b * ips + seg.item) * 2;
+      if (seg.t0 == 0) runs[0] = c;
+      if (seg.t1 == seg.nt) runs[1] = c;
+    }
     if (seg.t0 == 0 && seg.t1 == seg.nt) {
       float inv = L > 0.0f ? 1.0f / L : 0.0f;
       if (L != L) inv = L;
@@ -737,24 +742,16 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
   }
 }
 
-// The partials of one item: runs c0..c1 and their slots.
+// The partials of one item: runs c0..c0 + n - 1 and their slots.
 struct Parts {
   int c0, n, r;  // first run, number of runs, row in the block
   __device__ __forceinline__ int slot(int i) const { return 2 * (c0 + i) + (i == 0 ? 1 : 0); }
 };
-__device__ __forceinline__ Parts parts_of(const DecodeArgs& a, const DecodeWs& ws, int P0, int b, int h,
-                                          int rb, int kt) {
+__device__ __forceinline__ Parts parts_of(const DecodeArgs& a, const DecodeWs& ws, int b, int h, int rb) {
   const Shape& s = a.s;
   const int g = h / s.G, nrb = (s.G + rb - 1) / rb, r = h % s.G;
-  const long long T = ws.first[s.batch];
-  const int P = (int)min((long long)P0, T), nt = (seq_len(a, b) + kt - 1) / kt;
-  Parts p;
-  p.r = r % rb;
-  if (nt == 0) { p.c0 = p.n = 0; return p; }
-  const long long u0 = ws.first[b] + (long long)(g * nrb + r / rb) * nt;
-  p.c0 = run_of(u0, T, P);
-  p.n = run_of(u0 + nt - 1, T, P) - p.c0 + 1;
-  return p;
+  const int2 runs = reinterpret_cast<const int2*>(ws.runs)[(size_t)b * s.H_kv * nrb + g * nrb + r / rb];
+  return Parts{runs.x, runs.y - runs.x + 1, r % rb};
 }
 
 // Base-2 log-sum of one query row over its runs, by one warp.  A row finished
@@ -762,86 +759,147 @@ __device__ __forceinline__ Parts parts_of(const DecodeArgs& a, const DecodeWs& w
 __device__ __forceinline__ float row_lse2(const DecodeArgs& a, const DecodeWs& ws, const Parts& p, size_t row,
                                           int rb, int lane) {
   if (p.n == 1) return ws.lse2[row];
-  constexpr int N = (kMaxCtas + 31) / 32;
-  float2 v[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    v[i] = lane + 32 * i < p.n ? ws.pml[(size_t)p.slot(lane + 32 * i) * rb + p.r]
-                               : make_float2(-INFINITY, 0.0f);
   float M = -INFINITY, L = 0.0f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) M = fmaxf(M, v[i].x);
-  M = warp_max(M);
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (v[i].x != -INFINITY) L = fmaf(v[i].y, ex2_approx(v[i].x - M), L);
-  L = warp_sum(L);
-  return M + log2f(L);
+#pragma unroll 3
+  for (int i = lane; i < p.n; i += 32) {
+    const float2 v = ws.pml[(size_t)p.slot(i) * rb + p.r];
+    const float m = fmaxf(M, v.x);
+    if (m != -INFINITY) {
+      L = L * ex2_approx(M - m) + v.y * ex2_approx(v.x - m);
+      M = m;
+    }
+  }
+  const float top = warp_max(M);
+  L = warp_sum(top == -INFINITY ? L : L * ex2_approx(M - top));
+  return top + log2f(L);
 }
 
-// CTAs [0, batch * H): join the partials of one query row (or write an empty
-// sequence's row).  The others: masses of kMassChunk tokens at a time.
-template <typename T, int D>
-__global__ void __launch_bounds__(256)
-decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodeWs ws, int P0,
-                   int rb, int kt, int chunks) {
-  pdl_wait();
+// CTA `id` of the masses: one of `chunks` of a decision row.  A thread has
+// eight logits in flight, of 8 / QR tokens and QR rows.
+template <int QR>
+__device__ __forceinline__ void add_masses(const DecodeArgs& a, const DecodeWs& ws, int rb, int id,
+                                           int chunks) {
+  constexpr int NW = kJoinThreads / 32, TJ = 8 / QR;
+  __shared__ float s_lse[64];            // 64 rows at a time
   const Shape& s = a.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (blockIdx.x < s.batch * s.H) {
-    __shared__ float s_m[8], s_l[8], s_w[kMaxCtas];
-    __shared__ float4 s_o[256];
-    const int row = blockIdx.x, b = row / s.H;
-    const Parts p = parts_of(a, ws, P0, b, row % s.H, rb, kt);
-    if (p.n == 1) return;  // finished by its run
-    // a thread's outputs are under way while the weights are found: thread =
-    // (part group, four columns)
-    constexpr int CH = D / 4, GR = 256 / CH, U = 10;
-    const int col = tid % CH, grp = tid / CH;
-    const float4* po = reinterpret_cast<const float4*>(ws.po) + (size_t)p.r * CH + col;
-    const size_t step = (size_t)rb * CH;
-    float4 v[U];
+  const int bm = id / chunks, b = bm / a.n_mass, m = bm % a.n_mass;
+  const int rows = s.H / a.n_mass, h0 = m * rows;
+  const int first = (id % chunks) * TJ * kJoinThreads, step = chunks * TJ * kJoinThreads;
+  const int n = seq_len(a, b);
+  if (first >= n) return;
+  float* mass = a.tok_mass + ((size_t)b * a.n_mass + m) * s.L_ctx;
+  pdl_wait();
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += 64) {
+    const int nr = min(64, rows - r0);
+    const float decay = r0 == 0 ? a.decay : 1.0f;
+    const float* x = ws.logit + ((size_t)b * s.H + h0 + r0) * ws.Lp;
+    bool sums = false;
+#pragma unroll 1
+    for (int t0 = first; t0 < n; t0 += step) {
+      float old[TJ], sum[TJ];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = grp + u * GR;
-      v[u] = i < p.n ? po[p.slot(i) * step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
-    constexpr int N = (kMaxCtas + 255) / 256;
-    float2 ml[N];
-    float M = -INFINITY, L = 0.0f;
+      for (int j = 0; j < TJ; ++j) {
+        old[j] = decay != 0.0f ? mass[min(t0 + tid + j * kJoinThreads, n - 1)] : 0.0f;
+        sum[j] = 0.0f;
+      }
+#pragma unroll 1
+      for (int q0 = 0; q0 < nr; q0 += QR) {
+        float v[QR][TJ];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      ml[i] = tid + 256 * i < p.n ? ws.pml[(size_t)p.slot(tid + 256 * i) * rb + p.r]
-                                  : make_float2(-INFINITY, 0.0f);
-      M = fmaxf(M, ml[i].x);
-    }
-    M = warp_max(M);
-    if (lane == 0) s_m[warp] = M;
-    __syncthreads();
+        for (int q = 0; q < QR; ++q)
 #pragma unroll
-    for (int w = 0; w < 8; ++w) M = fmaxf(M, s_m[w]);
+          for (int j = 0; j < TJ; ++j)
+            v[q][j] = x[(size_t)min(q0 + q, nr - 1) * ws.Lp + min(t0 + tid + j * kJoinThreads, n - 1)];
+        if (!sums) {
+          sums = true;
+          __syncthreads();
+          for (int r = warp; r < nr; r += NW) {
+            const float lse = row_lse2(a, ws, parts_of(a, ws, b, h0 + r0 + r, rb),
+                                       (size_t)b * s.H + h0 + r0 + r, rb, lane);
+            if (lane == 0) s_lse[r] = lse == -INFINITY ? INFINITY : lse;  // no weight at all: 2^-inf
+          }
+          __syncthreads();
+        }
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float f = ml[i].x == -INFINITY ? 0.0f : ex2_approx(ml[i].x - M);
-      if (tid + 256 * i < p.n) s_w[tid + 256 * i] = f;
-      L = fmaf(ml[i].y, f, L);
-    }
-    L = warp_sum(L);
-    if (lane == 0) s_l[warp] = L;
-    __syncthreads();
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i0 = grp; i0 < p.n; i0 += U * GR) {
-      if (i0 != grp) {
+        for (int q = 0; q < QR; ++q) {
+          const float l2 = q0 + q < nr ? s_lse[q0 + q] : INFINITY;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = i0 + u * GR;
-          v[u] = i < p.n ? po[p.slot(i) * step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int j = 0; j < TJ; ++j) sum[j] += ex2_approx(v[q][j] - l2);
         }
       }
 #pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const int t = t0 + tid + j * kJoinThreads;
+        if (t < n) mass[t] = decay == 0.0f ? sum[j] : fmaf(decay, old[j], sum[j]);
+      }
+    }
+  }
+}
+
+// CTAs [0, batch * H): join the partials of one query row (or write an empty
+// sequence's row).  The others: masses, `chunks` CTAs a decision row.
+// Bound by latency: chains of dependent loads, and the first fetch of the
+// code, so loops are short rather than unrolled.  What depends on the lengths
+// alone is done before the wait for the main kernel; each chain's bulk loads
+// (partial outputs, logits) are issued ahead of the weights they wait for.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads, 4)
+decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodeWs ws, int rb,
+                   int chunks) {
+  const Shape& s = a.s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int NW = kJoinThreads / 32;
+  if (blockIdx.x < s.batch * s.H) {
+    __shared__ float s_m[NW], s_l[NW], s_w[kMaxCtas];
+    __shared__ float4 s_o[kJoinThreads];
+    constexpr int CH = D / 4, GR = kJoinThreads / CH, U = 5;
+    const int row = blockIdx.x, b = row / s.H, h = row % s.H;
+    const int n = seq_len(a, b);
+    const int col = tid % CH, grp = tid / CH;  // thread = (run group, four columns)
+    pdl_wait();
+    Parts p{0, 0, 0};
+    if (n > 0) p = parts_of(a, ws, b, h, rb);
+    if (p.n == 1) return;  // finished by its run
+    const float4* po = reinterpret_cast<const float4*>(ws.po) + (size_t)p.r * CH + col;
+    float4 v[U], o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float M = -INFINITY, L = 0.0f;
+#pragma unroll 1
+    for (int i0 = grp; i0 - grp < p.n; i0 += U * GR) {
+#pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * GR;
-        const float f = i < p.n ? s_w[i] : 0.0f;
+        const int i = min(i0 + u * GR, p.n - 1);  // the last run again, with no weight
+        v[u] = po[(size_t)p.slot(i) * rb * CH];
+      }
+      if (i0 == grp) {  // the runs' weights 2^(m - M)
+        constexpr int N = (kMaxCtas + kJoinThreads - 1) / kJoinThreads;
+        float2 ml[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          const int i = tid + q * kJoinThreads;
+          ml[q] = i < p.n ? ws.pml[(size_t)p.slot(i) * rb + p.r] : make_float2(-INFINITY, 0.0f);
+          M = fmaxf(M, ml[q].x);
+        }
+        M = warp_max(M);
+        if (lane == 0) s_m[warp] = M;
+        __syncthreads();
+        M = warp_max(s_m[lane % NW]);
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          const int i = tid + q * kJoinThreads;
+          const float f = ml[q].x == -INFINITY ? 0.0f : ex2_approx(ml[q].x - M);
+          if (i < p.n) s_w[i] = f;
+          L = fmaf(ml[q].y, f, L);
+        }
+        L = warp_sum(L);
+        if (lane == 0) s_l[warp] = L;
+        __syncthreads();
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float f = i0 + u * GR < p.n ? s_w[i0 + u * GR] : 0.0f;
+        if (i0 + u * GR >= p.n) continue;
         o.x = fmaf(f, v[u].x, o.x); o.y = fmaf(f, v[u].y, o.y);
         o.z = fmaf(f, v[u].z, o.z); o.w = fmaf(f, v[u].w, o.w);
       }
@@ -850,12 +908,14 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
     __syncthreads();
     if (tid < CH) {
       L = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) L += s_l[w];
-#pragma unroll
-      for (int i = 1; i < GR; ++i) {
-        const float4 x = s_o[i * CH + tid];
-        o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+      if (p.n > 0) {
+#pragma unroll 1
+        for (int w = 0; w < NW; ++w) L += s_l[w];
+#pragma unroll 1
+        for (int i = 1; i < GR; ++i) {
+          const float4 x = s_o[i * CH + tid];
+          o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+        }
       }
       float inv = L > 0.0f ? 1.0f / L : 0.0f;
       if (L != L) inv = L;
@@ -868,41 +928,11 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
     return;
   }
   // ---- masses
-  __shared__ float s_lse[32];
-  const int id = blockIdx.x - s.batch * s.H;
-  const int bm = id / chunks, b = bm / a.n_mass, m = bm % a.n_mass;
-  const int n = seq_len(a, b), rows = s.H / a.n_mass, h0 = m * rows;
-  constexpr int TU = kMassChunk / 256;
-  for (int t0 = (id % chunks) * kMassChunk; t0 < n; t0 += chunks * kMassChunk) {
-    float sum[TU], old[TU];
-    float* dst = a.tok_mass + ((size_t)b * a.n_mass + m) * s.L_ctx + t0 + tid;
-#pragma unroll
-    for (int j = 0; j < TU; ++j) {
-      sum[j] = 0.0f;
-      old[j] = a.decay != 0.0f && t0 + tid + 256 * j < n ? dst[256 * j] : 0.0f;
-    }
-    for (int r0 = 0; r0 < rows; r0 += 32) {
-      __syncthreads();
-      for (int r = r0 + warp; r < min(rows, r0 + 32); r += 8) {
-        const float lse = row_lse2(a, ws, parts_of(a, ws, P0, b, h0 + r, rb, kt),
-                                   (size_t)b * s.H + h0 + r, rb, lane);
-        if (lane == 0) s_lse[r - r0] = lse == -INFINITY ? INFINITY : lse;  // no weight at all: 2^-inf
-      }
-      __syncthreads();
-      const int nr = min(32, rows - r0);
-      const float* x = ws.logit + ((size_t)b * s.H + h0 + r0) * ws.Lp + t0 + tid;
-#pragma unroll 4
-      for (int q = 0; q < nr; ++q) {
-        const float l2 = s_lse[q];
-#pragma unroll
-        for (int j = 0; j < TU; ++j)
-          if (t0 + tid + 256 * j < n) sum[j] += ex2_approx(x[(size_t)q * ws.Lp + 256 * j] - l2);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < TU; ++j)
-      if (t0 + tid + 256 * j < n) dst[256 * j] = a.decay == 0.0f ? sum[j] : fmaf(a.decay, old[j], sum[j]);
-  }
+  const int id = blockIdx.x - s.batch * s.H, rows = s.H / a.n_mass;
+  if (rows > 4) add_masses<8>(a, ws, rb, id, chunks);
+  else if (rows > 2) add_masses<4>(a, ws, rb, id, chunks);
+  else if (rows > 1) add_masses<2>(a, ws, rb, id, chunks);
+  else add_masses<1>(a, ws, rb, id, chunks);
 }
 
 template <typename T, int D, int RB>
@@ -925,14 +955,22 @@ cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
   P = P < kMaxCtas ? P : kMaxCtas;
   P = (int)(most < P ? (most > 0 ? most : 1) : P);
   DL_LAUNCH(kern, P, kThreads, C::SMEM, st, mk, mv, a, w);
+  // masses: 1024 tokens a CTA, fewer while that leaves SMs idle (with two
+  // batches of loads a thread the join's first 3 us are shared; a batch's
+  // longest sequence must not take its time alone either)
   int chunks = 0;
   if (a.tok_mass && s.L_ctx > 0) {
-    chunks = (s.L_ctx + kMassChunk - 1) / kMassChunk;
+    const int rows = s.H / a.n_mass, tj = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8;
+    const int dec = s.batch * a.n_mass, fit = (4 * tc_sm_count() + dec - 1) / dec;
+    const int most = (s.L_ctx + kJoinThreads * tj - 1) / (kJoinThreads * tj);
+    const int few = (s.L_ctx + 1023) / 1024;
+    chunks = fit > few ? fit : few;
+    chunks = chunks < most ? chunks : most;
     chunks = chunks < 4096 ? chunks : 4096;
   }
   auto join = decode_join_kernel<T, D>;
-  DL_LAUNCH_DEPENDENT(join, s.batch * s.H + s.batch * a.n_mass * chunks, 256, 0, st, a, w, P, RB, C::KT,
-            chunks > 0 ? chunks : 1);
+  DL_LAUNCH_DEPENDENT(join, s.batch * s.H + s.batch * a.n_mass * chunks, kJoinThreads, 0, st, a, w, RB,
+                      chunks > 0 ? chunks : 1);
   return cudaGetLastError();
 }
 
