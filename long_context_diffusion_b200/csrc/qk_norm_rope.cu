@@ -56,6 +56,40 @@ template <> struct Vec4<__nv_bfloat16> {
   }
 };
 
+// Row of KV head 0 of token i of sequence b in the pools, or -1 (no cache, or
+// the token is not appended).  The CTA that reports also writes the token's
+// bookkeeping and, for the first token, the sequence's new end.
+__device__ __forceinline__ long long cache_row(const RopeArgs& a, int b, int i, bool report) {
+  if (!a.start) return -1;
+  const Shape& s = a.s;
+  const int st = a.start[b];
+  const bool fits = st >= 0 && (long long)st + a.n_tok <= s.L_ctx;
+  if (report && i == 0) {
+    if (!fits) flag_error(a.err, ERR_BAD_INDEX);
+    if (a.end) a.end[b] = fits ? st + a.n_tok : st;
+  }
+  if (!fits) return -1;
+  const int t = st + i, slot = a.page_table[(size_t)b * s.n_pages + t / 64];
+  if (slot < 0 || slot >= s.n_slots) {
+    if (report) flag_error(a.err, ERR_BAD_INDEX);
+    return -1;
+  }
+  if (report) {
+    for (int m = 0; m < a.n_mass; ++m) {
+      const size_t e = ((size_t)b * a.n_mass + m) * s.L_ctx + t;
+      if (a.tok_pos) a.tok_pos[e] = a.pos[(size_t)b * a.n_tok + i];
+      if (a.tok_mass) a.tok_mass[e] = 0.0f;
+    }
+  }
+  return (long long)slot * s.H_kv * 64 + (t % 64);
+}
+
+// Sine and cosine of a position's turn at frequency j.
+__device__ __forceinline__ void turn(const RopeArgs& a, size_t tok, int j, float* sn, float* cs) {
+  const double turns = (double)a.pos[tok] * (double)a.inv_freq[j] * 0.15915494309189533577;
+  sincospif(2.0f * (float)(turns - rint(turns)), sn, cs);
+}
+
 template <typename T, int D, int TT, int U>
 __global__ void __launch_bounds__(kRopeThreads)
 qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int tiles, int rows_per_cta) {
@@ -107,38 +141,9 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int tiles, int rows_per_
     if (it0 == 0) {
       for (int e = tid; e < n_tok * half; e += kRopeThreads) {
         const int t = e / half, j = e - t * half;
-        const double turns = (double)a.pos[tok0 + t] * (double)a.inv_freq[j] * 0.15915494309189533577;
-        sincospif(2.0f * (float)(turns - rint(turns)), reinterpret_cast<float*>(s_sin[t]) + j,
-                  reinterpret_cast<float*>(s_cos[t]) + j);
+        turn(a, tok0 + t, j, reinterpret_cast<float*>(s_sin[t]) + j, reinterpret_cast<float*>(s_cos[t]) + j);
       }
-      if (tid < n_tok) {                     // the token's place in the cache
-        long long row = -1;
-        if (a.start) {
-          const int st = a.start[b];
-          const bool fits = st >= 0 && (long long)st + a.n_tok <= s.L_ctx;
-          if (blockIdx.y == 0 && i0 == 0 && tid == 0) {
-            if (!fits) flag_error(a.err, ERR_BAD_INDEX);
-            if (a.end) a.end[b] = fits ? st + a.n_tok : st;
-          }
-          if (fits) {
-            const int t = st + i0 + tid;
-            const int slot = a.page_table[(size_t)b * s.n_pages + t / 64];
-            if (slot < 0 || slot >= s.n_slots) {
-              if (blockIdx.y == 0) flag_error(a.err, ERR_BAD_INDEX);
-            } else {
-              row = (long long)slot * s.H_kv * 64 + (t % 64);
-              if (blockIdx.y == 0) {
-                for (int m = 0; m < a.n_mass; ++m) {
-                  const size_t e = ((size_t)b * a.n_mass + m) * s.L_ctx + t;
-                  if (a.tok_pos) a.tok_pos[e] = a.pos[tok0 + tid];
-                  if (a.tok_mass) a.tok_mass[e] = 0.0f;
-                }
-              }
-            }
-          }
-        }
-        s_row[tid] = row;
-      }
+      if (tid < n_tok) s_row[tid] = cache_row(a, b, i0 + tid, blockIdx.y == 0);
       __syncthreads();
     }
 #pragma unroll
@@ -204,6 +209,248 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int tiles, int rows_per_
   }
 }
 
+// ---- long prompts: eight tokens a CTA and all their rows, a thread keeping to
+// its token and columns.
+//
+// With the kernel above the instructions, not HBM, set the time of a prompt
+// (176 for two rows of a warp, 62 of 91 us).  Here a thread holds two runs of
+// eight columns (off0.. and off1.., 16-byte loads) of one token and walks the
+// heads, so that the row's coefficients stay in registers with the norm's
+// weights multiplied in,
+//   y_u' = inv (x_u (w_u cos) - x_v (w_v sin)),
+//   y_v' = inv (x_v (w_v cos) + x_u (w_u sin)),
+// and pairs of columns share an instruction (f32x2).
+__device__ __forceinline__ unsigned long long pack2(float x, float y) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b,
+                                                   unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Eight consecutive values as loaded.
+template <typename T> struct Oct;
+template <> struct Oct<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ void get(unsigned long long (&x)[4]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ void set(const unsigned long long (&x)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack2(x[i]);
+      w[i] = pack_bf16x2(f.x, f.y);
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <> struct Oct<float> {
+  float4 v[2];
+  __device__ __forceinline__ void load(const float* p) {
+    v[0] = *reinterpret_cast<const float4*>(p);
+    v[1] = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    *reinterpret_cast<float4*>(p) = v[0];
+    *reinterpret_cast<float4*>(p + 4) = v[1];
+  }
+  __device__ __forceinline__ void get(unsigned long long (&x)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[2 * i] = pack2(v[i].x, v[i].y);
+      x[2 * i + 1] = pack2(v[i].z, v[i].w);
+    }
+  }
+  __device__ __forceinline__ void set(const unsigned long long (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 p = unpack2(x[2 * i]), q = unpack2(x[2 * i + 1]);
+      v[i] = make_float4(p.x, p.y, q.x, q.y);
+    }
+  }
+};
+
+constexpr int kWideTokens = 8, kWideThreads = 128;
+
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kWideThreads, 4)
+qk_norm_rope_wide_kernel(const __grid_constant__ RopeArgs a, int tiles) {
+  constexpr int TT = kWideTokens, TPR = D / 16;       // threads per row
+  constexpr int GR = kWideThreads / (TT * TPR);       // heads taken at a time
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;           // rows loaded ahead
+  __shared__ float s_cos[TT][D / 2], s_sin[TT][D / 2];
+  __shared__ long long s_row[TT];
+  const Shape& s = a.s;
+  const int tid = threadIdx.x, c = tid % TPR, t = (tid / TPR) % TT, grp = tid / (TPR * TT);
+  const int b = blockIdx.x / tiles, i0 = (blockIdx.x - b * tiles) * TT;
+  const int n_tok = min(TT, a.n_tok - i0), half = a.rot_dim / 2;
+  const size_t tok0 = (size_t)b * a.n_tok + i0;
+  const bool live = t < n_tok;
+  // columns: off0 .. + 7 and off1 .. + 7; rotated pairs, or columns left alone
+  int off0, off1;
+  bool rotated;
+  if (INTER) {
+    off0 = 16 * c;
+    off1 = off0 + 8;
+    rotated = off0 < a.rot_dim;
+  } else if (8 * c < half) {
+    off0 = 8 * c;
+    off1 = half + off0;
+    rotated = true;
+  } else {
+    off0 = a.rot_dim + 8 * c - half;
+    off1 = off0 + (D - a.rot_dim) / 2;
+    rotated = false;
+  }
+  pdl_trigger();
+  pdl_wait();
+  for (int e = tid; e < n_tok * half; e += kWideThreads) {
+    const int tt = e / half, j = e - tt * half;
+    turn(a, tok0 + tt, j, &s_sin[tt][j], &s_cos[tt][j]);
+  }
+  if (tid < n_tok) s_row[tid] = cache_row(a, b, i0 + tid, true);
+  __syncthreads();
+  const long long row = live ? s_row[t] : -1;
+  // a token past the last reads the last one's rows and writes nothing
+  const T* src = reinterpret_cast<const T*>(a.qkv) + (tok0 + min(t, n_tok - 1)) * a.qkv_stride;
+#pragma unroll 1
+  for (int kind = 0; kind < 3; ++kind) {              // query, key, value heads
+    const int n = kind == 0 ? s.H : s.H_kv;
+    const int h0 = kind == 0 ? 0 : kind == 1 ? s.H : s.H + s.H_kv;
+    T* out = reinterpret_cast<T*>(kind == 0 ? a.Q_out : kind == 1 ? a.K_out : a.V_out);
+    if (out) out += ((size_t)b * n * a.n_tok + i0 + t) * D;
+    T* pool = nullptr;
+    if (kind > 0 && row >= 0) pool = reinterpret_cast<T*>(kind == 1 ? a.K_pool : a.V_pool) + row * D;
+    const T* x0 = src + (size_t)h0 * D;
+    const T* w = reinterpret_cast<const T*>(kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr);
+    // coefficients of the two runs: out0 = x0 A + other B, out1 = x1 C + other D
+    unsigned long long A[4], B[4], C[4], E[4];
+    if (kind < 2) {
+      unsigned long long w0[4], w1[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w0[i] = w1[i] = pack2(1.0f, 1.0f);
+      if (w) {
+        Oct<T> o;
+        o.load(w + off0);
+        o.get(w0);
+        o.load(w + off1);
+        o.get(w1);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = unpack2(w0[i]), q = unpack2(w1[i]);
+        float c0 = 1.0f, c1 = 1.0f, c2 = 1.0f, c3 = 1.0f, s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+        if (rotated && live) {
+          if (INTER) {                                // pair i of each run
+            c0 = c1 = s_cos[t][8 * c + i]; s0 = s1 = s_sin[t][8 * c + i];
+            c2 = c3 = s_cos[t][8 * c + 4 + i]; s2 = s3 = s_sin[t][8 * c + 4 + i];
+          } else {
+            c0 = c2 = s_cos[t][8 * c + 2 * i]; s0 = s2 = s_sin[t][8 * c + 2 * i];
+            c1 = c3 = s_cos[t][8 * c + 2 * i + 1]; s1 = s3 = s_sin[t][8 * c + 2 * i + 1];
+          }
+        }
+        A[i] = pack2(p.x * c0, p.y * c1);
+        C[i] = pack2(q.x * c2, q.y * c3);
+        // what the partner adds: its own weight, minus for the first of a pair
+        B[i] = INTER ? pack2(-p.y * s0, p.x * s1) : pack2(-q.x * s0, -q.y * s1);
+        E[i] = INTER ? pack2(-q.y * s2, q.x * s3) : pack2(p.x * s2, p.y * s3);
+      }
+    }
+    Oct<T> v0[U], v1[U];                              // rows under way: a rolling window
+    auto fetch = [&](int u, int h) {
+      const T* x = x0 + (size_t)min(h, n - 1) * D;
+      v0[u].load(x + off0);
+      v1[u].load(x + off1);
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) fetch(u, grp + u * GR);
+#pragma unroll 1
+    for (int r = grp; r - grp < n; r += U * GR) {  // uniform over the CTA
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (kind < 2) {
+          unsigned long long x[4], y[4];
+          v0[u].get(x);
+          v1[u].get(y);
+          unsigned long long inv = pack2(1.0f, 1.0f);
+          if (w) {
+            unsigned long long sq = mul2(x[0], x[0]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) sq = fma2(x[i], x[i], sq);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sq = fma2(y[i], y[i], sq);
+            const float2 f = unpack2(sq);
+            float q = f.x + f.y;
+#pragma unroll
+            for (int o = TPR / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+            const float z = __frsqrt_rn(q * (1.0f / D) + a.eps);
+            inv = pack2(z, z);
+          }
+          unsigned long long p[4], q[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[i] = mul2(x[i], A[i]);
+            q[i] = mul2(y[i], C[i]);
+          }
+          if (rotated) {                              // else the partner's values must not reach it
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (INTER) {
+                const float2 f = unpack2(x[i]), g = unpack2(y[i]);
+                p[i] = fma2(pack2(f.y, f.x), B[i], p[i]);
+                q[i] = fma2(pack2(g.y, g.x), E[i], q[i]);
+              } else {
+                p[i] = fma2(y[i], B[i], p[i]);
+                q[i] = fma2(x[i], E[i], q[i]);
+              }
+            }
+          }
+          if (w) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { p[i] = mul2(p[i], inv); q[i] = mul2(q[i], inv); }
+          }
+          v0[u].set(p);
+          v1[u].set(q);
+        }
+        const int h = r + u * GR;
+        if (h < n && live) {
+          if (out) {
+            T* o = out + (size_t)h * a.n_tok * D;
+            v0[u].store(o + off0);
+            v1[u].store(o + off1);
+          }
+          if (pool) {
+            T* o = pool + (size_t)h * 64 * D;
+            v0[u].store(o + off0);
+            v1[u].store(o + off1);
+          }
+        }
+        fetch(u, h + U * GR);
+      }
+    }
+  }
+}
+
 template <typename T, int D>
 cudaError_t run_rope(const RopeArgs& a, cudaStream_t st) {
   const Shape& s = a.s;
@@ -214,6 +461,15 @@ cudaError_t run_rope(const RopeArgs& a, cudaStream_t st) {
   const int tt = a.n_tok >= 8 ? 8 : 1;
   const int tiles = (a.n_tok + tt - 1) / tt;
   const long long all = (long long)s.batch * tiles, want = 6ll * tc_sm_count();
+  // Enough tokens to fill the GPU without splitting their rows, and runs of
+  // eight columns that are rotated or left alone as a whole.
+  if (tt == 8 && all >= 2ll * tc_sm_count() && a.rot_dim % 16 == 0) {
+    if (a.interleaved)
+      DL_LAUNCH((qk_norm_rope_wide_kernel<T, D, true>), (unsigned)all, kWideThreads, 0, st, a, tiles);
+    else
+      DL_LAUNCH((qk_norm_rope_wide_kernel<T, D, false>), (unsigned)all, kWideThreads, 0, st, a, tiles);
+    return cudaGetLastError();
+  }
   const int most = (n_rows * tt + RPP - 1) / RPP;
   long long split = all < want ? (want + all - 1) / all : 1;
   split = split < most ? split : most;

@@ -88,6 +88,14 @@ ROPE_CASES = [
     ("bf16", 128, 3, 1, 4, 2, 0, True, False, 0),
     ("fp32", 64, 5, 5, 130, 2, 48, True, False, 0),
     ("bf16", 128, 16, 8, 300, 4, 128, True, False, 128),
+    # enough tokens for the long-prompt kernel (at least 2 x 148 groups of eight)
+    ("bf16", 128, 5, 1, 2373, 1, 128, True, False, 0),
+    ("bf16", 64, 4, 2, 1203, 2, 32, True, False, 8),
+    ("bf16", 128, 2, 2, 803, 3, 96, False, True, 0),
+    ("bf16", 64, 1, 1, 2401, 1, 0, True, False, 0),
+    ("bf16", 128, 2, 1, 2404, 1, 40, True, False, 0),    # 40: by fours
+    ("fp32", 128, 3, 1, 1201, 2, 128, True, True, 4),
+    ("fp32", 64, 4, 2, 2369, 1, 64, False, False, 0),
 ]
 
 
