@@ -555,6 +555,9 @@ dl_status dl_cache_compact(const dl_attn_desc* desc, const int32_t* hole_idx,
     return fail(DL_ERR_INVALID_ARG, "dl_cache_compact: NULL pointer");
   if (!aligned16(K_pool) || !aligned16(V_pool))
     return fail(DL_ERR_INVALID_ARG, "dl_cache_compact: pools must be 16-byte aligned");
+  if ((long long)s.n_slots * s.H_kv * s.page >= (1ll << 31))
+    return fail(DL_ERR_UNSUPPORTED, "dl_cache_compact: pool of %lld rows (need < 2^31)",
+                (long long)s.n_slots * s.H_kv * s.page);
   if (!mass_rows_ok(s, n_mass))
     return fail(DL_ERR_INVALID_ARG, "n_mass=%d (need 1 or H_kv=%d)", n_mass, s.H_kv);
   unsigned* err = nullptr;

@@ -447,9 +447,9 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int max_it) {
   if (tid == 0 && rank == 0) a.move_cnt[row] = moves;
 }
 
-// A warp task is 32 moves of one (decision row, KV head).  CH: 16-byte pieces
+// A warp task is M moves of one (decision row, KV head).  CH: 16-byte pieces
 // of a row.
-template <int CH>
+template <int CH, int M>
 __global__ void __launch_bounds__(256)
 cache_compact_kernel(const __grid_constant__ CompactArgs a, int groups, long long tasks) {
   constexpr int PER = 2 * CH;            // pieces of a move, K then V
@@ -467,26 +467,29 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, int groups, long lon
     const long long rh = task / groups;
     const int row = (int)(rh / heads), hd = (int)(rh % heads);
     const int b = row / a.n_mass, g = a.n_mass == 1 ? hd : row % a.n_mass;
+    // the moves do not wait for their number (their lists are max_move long)
+    const int i = grp * M + lane;
+    const bool in = lane < M && i < a.max_move;
+    const size_t at = (size_t)row * a.max_move + (in ? i : 0);
+    const int to = a.hole_idx[at], from = a.fill_idx[at];
     int cnt = a.move_cnt[row];
     if (cnt < 0 || cnt > a.max_move) {
       if (grp == 0 && hd == 0 && lane == 0) flag_error(a.err, ERR_BAD_INDEX);
       cnt = cnt < 0 ? 0 : a.max_move;
     }
-    const int left = cnt - grp * 32;
-    if (left <= 0) continue;
-    // lane = move
-    long long src = -1, dst = -1;        // 16-byte pieces from the pools' start; -1: no move
-    if (lane < left) {
-      const size_t at = (size_t)row * a.max_move + grp * 32 + lane;
-      const int to = a.hole_idx[at], from = a.fill_idx[at];
+    const int n = min(M, cnt - grp * M);
+    if (n <= 0) continue;
+    // lane = move; rows of the pools, -1: no move
+    int src = -1, dst = -1;
+    if (lane < n) {
       bool ok = to >= 0 && to < s.L_ctx && from >= 0 && from < s.L_ctx;
       if (ok) {
         const int32_t* table = a.page_table + (size_t)b * s.n_pages;
         const int st = table[to / 64], sf = table[from / 64];
         ok = st >= 0 && st < s.n_slots && sf >= 0 && sf < s.n_slots;
         if (ok) {
-          dst = (((long long)st * s.H_kv + g) * 64 + to % 64) * CH;
-          src = (((long long)sf * s.H_kv + g) * 64 + from % 64) * CH;
+          dst = (st * s.H_kv + g) * 64 + to % 64;
+          src = (sf * s.H_kv + g) * 64 + from % 64;
           if (hd == 0) {
             const size_t o = (size_t)row * s.L_ctx;
             if (a.tok_pos) a.tok_pos[o + to] = a.tok_pos[o + from];
@@ -496,23 +499,18 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, int groups, long lon
       }
       if (!ok && hd == 0) flag_error(a.err, ERR_BAD_INDEX);
     }
-    const int n = min(32, left);
 #pragma unroll 1
     for (int p0 = 0; p0 < n * PER; p0 += 32 * U) {
       uint4 v[U];
-      long long to[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int p = p0 + 32 * u + lane, mv = p / PER, c = p % CH;
-        const long long f = __shfl_sync(0xffffffffu, src, mv & 31);
-        const long long t = __shfl_sync(0xffffffffu, dst, mv & 31);
-        to[u] = mv < n && t >= 0 ? t + c : -1;
-        if (to[u] >= 0) v[u] = (p / CH) % 2 ? Vp[f + c] : Kp[f + c];
+        const int p = p0 + 32 * u + lane, f = __shfl_sync(0xffffffffu, src, (p / PER) & 31);
+        if (p < n * PER && f >= 0) v[u] = ((p / CH) % 2 ? Vp : Kp)[(size_t)f * CH + p % CH];
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int p = p0 + 32 * u + lane;
-        if (to[u] >= 0) ((p / CH) % 2 ? Vp : Kp)[to[u]] = v[u];
+        const int p = p0 + 32 * u + lane, t = __shfl_sync(0xffffffffu, dst, (p / PER) & 31);
+        if (p < n * PER && t >= 0) ((p / CH) % 2 ? Vp : Kp)[(size_t)t * CH + p % CH] = v[u];
       }
     }
   }
@@ -559,18 +557,23 @@ cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st) {
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {
   if (a.max_move == 0) return cudaSuccess;
   const Shape& s = a.s;
-  const int groups = (a.max_move + 31) / 32, heads = a.n_mass == 1 ? s.H_kv : 1;
-  const long long tasks = (long long)s.batch * a.n_mass * heads * groups;
-  const long long want = (tasks + 7) / 8, most = (long long)tc_sm_count() * 8;
+  const long long rows = (long long)s.batch * a.n_mass * (a.n_mass == 1 ? s.H_kv : 1);
+  // Eight moves a warp (one round of loads) while that leaves SMs idle, else 32.
+  const int sms = tc_sm_count(), few = (a.max_move + 31) / 32;
+  const bool wide = rows * few >= 20ll * sms;
+  const int groups = wide ? few : (a.max_move + 7) / 8;
+  const long long tasks = rows * groups, want = (tasks + 7) / 8, most = (long long)sms * 8;
   const int grid = (int)(want < most ? want : most);
+#define DL_COMPACT(CH_)                                                                           \
+  do {                                                                                            \
+    if (wide) DL_LAUNCH((cache_compact_kernel<CH_, 32>), grid, 256, 0, st, a, groups, tasks);     \
+    else DL_LAUNCH((cache_compact_kernel<CH_, 8>), grid, 256, 0, st, a, groups, tasks);           \
+  } while (0)
   const int pieces = s.d * (s.dtype == DL_BF16 ? 2 : 4) / 16;
-  if (pieces == 8) {
-    DL_LAUNCH(cache_compact_kernel<8>, grid, 256, 0, st, a, groups, tasks);
-  } else if (pieces == 16) {
-    DL_LAUNCH(cache_compact_kernel<16>, grid, 256, 0, st, a, groups, tasks);
-  } else {
-    DL_LAUNCH(cache_compact_kernel<32>, grid, 256, 0, st, a, groups, tasks);
-  }
+  if (pieces == 8) DL_COMPACT(8);
+  else if (pieces == 16) DL_COMPACT(16);
+  else DL_COMPACT(32);
+#undef DL_COMPACT
   return cudaGetLastError();
 }
 
