@@ -7,10 +7,11 @@
 // Bound: latency and instruction issue (a row of n tokens is 8 n bytes; 128
 // rows of 32K, 38 MB, are 6 us of HBM; every instruction a token takes is 1 us
 // there, so tokens are handled four at a time where they can be).  A decision
-// row is taken by a cluster of 1 to 8 CTAs that splits its n tokens evenly in
-// index order.  A warp reads its tokens coalesced, 16 bytes a lane, and turns
-// them through shared memory so that each lane ends with `it` consecutive
-// tokens; their keys stay there, masses and positions are read once.
+// row is taken by a cluster of 1 to 8 CTAs that splits the row's capacity
+// evenly in index order, 4 CPL tokens a thread.  A warp reads its tokens
+// coalesced, 16 bytes a lane, and turns them through shared memory so that
+// each lane ends with consecutive tokens; their keys stay there, masses and
+// positions are read once.
 //  - The budget-th key by radix select: a histogram of the top 12 bits (sign,
 //    exponent, three bits of mantissa), then of the next 10 and the last 10
 //    among the keys that share the digits found.  Each CTA counts its own
@@ -18,8 +19,9 @@
 //    sums over the cluster, finds the group, and adds that group's 32 bins
 //    alone (adding all bins over the cluster took four times as long).  The
 //    search ends at the first digit whose whole bin stays.
-//  - A lane's keep bits are one word; holes and fills are counted and listed
-//    by words, with prefix sums over lanes, warps and CTAs.
+//  - A lane's keep bits are one word; holes and fills are counted by words,
+//    with prefix sums over lanes, warps and CTAs, listed in shared memory and
+//    copied out side by side.
 // Rows too long for the cluster's shared memory go through it in tiles, read
 // again for every pass.
 //
@@ -38,7 +40,7 @@ namespace {
 constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxIt = 44;               // most tokens of a thread: 11 16-byte chunks, 176 KB a CTA
+constexpr int kMaxChunks = 8;            // 16-byte chunks of a thread
 constexpr unsigned kHeldKey = 0xFF800000u;  // the key of +infinity
 
 // Order-preserving bits of a mass: a < b as numbers <=> key(a) < key(b);
@@ -75,33 +77,14 @@ __device__ __forceinline__ int warp_inclusive(int v, int lane) {
   return v;
 }
 
-// Lists the set bits of the lanes' words, in order, from out[at] on; bit i of
-// lane l is token t0 + i of that lane.  Word by word, so that neighbours are
-// written together, or each lane its own when no word is crowded.
-__device__ __forceinline__ int list_bits(unsigned long long w, int32_t* out, int at, long long t0,
-                                         int it, int lane) {
-  const int c = __popcll(w), upto = warp_inclusive(c, lane);
-  if (__reduce_max_sync(0xffffffffu, c) <= 12) {
-    int32_t* o = out + at + upto - c;
-    for (; w; w &= w - 1) *o++ = (int32_t)(t0 + __ffsll(w) - 1);
-  } else {
-    for (unsigned some = __ballot_sync(0xffffffffu, w != 0ull); some; some &= some - 1) {
-      const int j = __ffs(some) - 1;
-      const unsigned long long v = __shfl_sync(0xffffffffu, w, j);
-      const int o = at + __shfl_sync(0xffffffffu, upto - c, j);
-      const long long t = __shfl_sync(0xffffffffu, t0, j);
-      for (int i = lane; i < it; i += 32)
-        if ((v >> i) & 1) out[o + __popcll(v & ((1ull << i) - 1))] = (int32_t)(t + i);
-    }
-  }
-  return at + __shfl_sync(0xffffffffu, upto, 31);
-}
-
-// VEC: masses and positions may be read 16 bytes at a time.
-template <bool VEC>
+// CPL: 16-byte chunks (four tokens) of a thread.  VEC: masses and positions may
+// be read 16 bytes at a time.
+template <int CPL, bool VEC>
 __global__ void __launch_bounds__(kEvThreads, 1)
-evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int max_it) {
-  extern __shared__ uint4 s_key[];       // [thread][it / 4 | 1]
+evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
+  constexpr int IT = 4 * CPL;            // tokens of a thread
+  constexpr int PITCH = CPL | 1;         // chunks from lane to lane: odd, to spread the banks
+  extern __shared__ uint4 s_key[];       // [thread][PITCH], later the lists
   __shared__ __align__(16) int s_hist[4096 + 2 * 1024];
   __shared__ int s_group[3][128];        // this CTA's counts of 32 bins
   __shared__ int s_gsum[128], s_bsum[32];  // the cluster's
@@ -125,76 +108,55 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int max_it) {
   int32_t* fill = a.fill_idx + (size_t)row * a.max_move;
   int moves = 0;
   if (!bad && n > a.budget) {            // the same for the whole cluster
-    const float* mass = a.tok_mass + (size_t)row * s.L_ctx;
-    const int32_t* pos = a.tok_pos ? a.tok_pos + (size_t)row * s.L_ctx : nullptr;
-    // Tokens per thread of a tile, a multiple of 4; tiles; the tile's first
-    // token of this warp.  64 bits: the last ones may lie past 2^31.
-    const int span = cs * kEvThreads;
-    int it = (int)(((long long)n + 4 * span - 1) / (4 * span)) * 4, tiles = 1;
-    if (it > max_it) {
-      tiles = (it + max_it - 1) / max_it;
-      it = max_it;
-    }
-    const int cpl = it / 4, pitch = cpl | 1;  // chunks of a lane; an odd pitch spreads the banks
-    uint4* warp_keys = s_key + warp * 32 * pitch;
-    uint4* my_keys = warp_keys + lane * pitch;
-    auto warp_at = [&](int k) {
-      return (((long long)rank * tiles + k) * kEvWarps + warp) * 32 * it;
-    };
-    // chunk q (16 bytes) of a warp's tile belongs to lane q / cpl
-    const int step_l = 32 / cpl, step_c = 32 % cpl;
-    struct Spot { int l, c; };
-    auto first_spot = [&]() { return Spot{lane / cpl, lane % cpl}; };
-    auto next_spot = [&](Spot& p) {
-      p.l += step_l;
-      p.c += step_c;
-      if (p.c >= cpl) { p.c -= cpl; ++p.l; }
-    };
-    // four values at token t (a chunk behind the row's end repeats its last)
-    auto load4 = [&](const int* x, long long t) -> int4 {
-      if (VEC) return *reinterpret_cast<const int4*>(x + min(t, (long long)((n - 1) & ~3)));
+    const int* mass = reinterpret_cast<const int*>(a.tok_mass + (size_t)row * s.L_ctx);
+    const int* pos = a.tok_pos ? a.tok_pos + (size_t)row * s.L_ctx : nullptr;
+    const unsigned len = (unsigned)n;
+    // this warp's first token of tile k (unsigned: the last may lie past 2^31)
+    auto warp_at = [&](int k) { return (unsigned)((rank * tiles + k) * kEvWarps + warp) * (32u * IT); };
+    // four values from token t on; behind the row's end, its last ones
+    auto load4 = [&](const int* x, unsigned t) -> int4 {
+      if (VEC) return *reinterpret_cast<const int4*>(x + min(t, (len - 1u) & ~3u));
       int4 v;
-      v.x = x[min(t, (long long)n - 1)];
-      v.y = x[min(t + 1, (long long)n - 1)];
-      v.z = x[min(t + 2, (long long)n - 1)];
-      v.w = x[min(t + 3, (long long)n - 1)];
+      v.x = x[min(t, len - 1u)];
+      v.y = x[min(t + 1u, len - 1u)];
+      v.z = x[min(t + 2u, len - 1u)];
+      v.w = x[min(t + 3u, len - 1u)];
       return v;
     };
-    auto load_pos = [&](long long t) -> int4 {
+    auto load_pos = [&](unsigned t) -> int4 {
       return pos ? load4(pos, t) : make_int4((int)t, (int)t + 1, (int)t + 2, (int)t + 3);
     };
-    const int* massi = reinterpret_cast<const int*>(mass);
-    constexpr int U = 4;                 // 16-byte loads ahead
-    int4 m0[U];                          // the first masses do not wait for the largest position
-    if (tiles == 1) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) m0[u] = load4(massi, warp_at(0) + 4 * (32 * u + lane));
-    }
+    // chunk 32 i + lane of a warp's tile belongs to lane (32 i + lane) / CPL
+    uint4* warp_keys = s_key + warp * 32 * PITCH;
+    uint4* my_keys = warp_keys + lane * PITCH;
+    uint4* put_at = warp_keys + (lane / CPL) * PITCH + lane % CPL;
+    constexpr int PUT = (32 / CPL) * PITCH;  // from chunk to chunk of the loading order
+
+    // ---- largest position
     int last = INT32_MIN;
+#pragma unroll 1
     for (int k = 0; k < tiles; ++k) {
-      const long long t0 = warp_at(k) + 4 * lane;
-      Spot sp = first_spot();
-      for (int i0 = 0; i0 < cpl; i0 += U) {
-        if (warp_at(k) + 128 * i0 >= n) break;
-        int4 p[U];
+      const unsigned t0 = warp_at(k) + 4u * lane;
+      if (warp_at(k) >= len) break;
+      int4 p[CPL];
 #pragma unroll
-        for (int u = 0; u < U; ++u) p[u] = load_pos(t0 + 128 * (i0 + u));
+      for (int i = 0; i < CPL; ++i) p[i] = load_pos(t0 + 128u * i);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const long long t = t0 + 128 * (i0 + u);
-          if (t + 3 < n) {
-            last = max(max(max(last, p[u].x), max(p[u].y, p[u].z)), p[u].w);
-          } else {
-            if (t < n) last = max(last, p[u].x);
-            if (t + 1 < n) last = max(last, p[u].y);
-            if (t + 2 < n) last = max(last, p[u].z);
-          }
-          if (tiles == 1 && i0 + u < cpl) {
-            warp_keys[sp.l * pitch + sp.c] = make_uint4(p[u].x, p[u].y, p[u].z, p[u].w);
-            next_spot(sp);
-          }
-        }
+      for (int i = 0; i < CPL; ++i) {
+        const unsigned t = t0 + 128u * i;
+        if (t < len) last = max(last, p[i].x);
+        if (t + 1u < len) last = max(last, p[i].y);
+        if (t + 2u < len) last = max(last, p[i].z);
+        if (t + 3u < len) last = max(last, p[i].w);
+        if (tiles == 1) put_at[i * PUT] = make_uint4(p[i].x, p[i].y, p[i].z, p[i].w);
       }
+    }
+    constexpr int U = CPL < 4 ? CPL : 4;   // masses loaded ahead
+    const bool here = warp_at(0) < len;
+    int4 m0[U];                          // the first do not wait for the largest position
+    if (tiles == 1 && here) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) m0[u] = load4(mass, warp_at(0) + 4u * lane + 128u * u);
     }
     last = __reduce_max_sync(0xffffffffu, last);
     if (lane == 0) s_max[warp] = last;
@@ -211,42 +173,39 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int max_it) {
     auto key_of = [&](int p, int m) {
       return (unsigned)p - (unsigned)a.n_first < loose ? mass_key(__int_as_float(m)) : kHeldKey;
     };
-    // Keys of tile k, each lane's own chunks in order (0: no token).
+    // Keys of tile k, each lane's own chunks in order (0: no token).  False:
+    // the warp has none.
     auto load_tile = [&](int k) {
-      const long long t0 = warp_at(k) + 4 * lane;
-      Spot sp = first_spot();
+      const unsigned w0 = warp_at(k), t0 = w0 + 4u * lane;
+      if (w0 >= len) return false;
       __syncwarp();
 #pragma unroll 1
-      for (int i0 = 0; i0 < cpl; i0 += U) {
-        const bool none = warp_at(k) + 128 * i0 >= n;  // nothing here for the warp
-        if (!none && (i0 > 0 || tiles > 1)) {
+      for (int i0 = 0; i0 < CPL; i0 += U) {
+        if (i0 > 0 || tiles > 1) {
 #pragma unroll
-          for (int u = 0; u < U; ++u) m0[u] = load4(massi, t0 + 128 * (i0 + u));
+          for (int u = 0; u < U; ++u) m0[u] = load4(mass, t0 + 128u * (i0 + u));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (i0 + u >= cpl) break;
-          const long long t = t0 + 128 * (i0 + u);
-          uint4* at = warp_keys + sp.l * pitch + sp.c;
-          uint4 q = make_uint4(0u, 0u, 0u, 0u);
-          if (t < n) {
-            int4 p;
-            if (tiles == 1) {
-              const uint4 v = *at;
-              p = make_int4(v.x, v.y, v.z, v.w);
-            } else {
-              p = load_pos(t);
-            }
-            q.x = key_of(p.x, m0[u].x);
-            if (t + 1 < n) q.y = key_of(p.y, m0[u].y);
-            if (t + 2 < n) q.z = key_of(p.z, m0[u].z);
-            if (t + 3 < n) q.w = key_of(p.w, m0[u].w);
+          const unsigned t = t0 + 128u * (i0 + u);
+          uint4* at = put_at + (i0 + u) * PUT;
+          int4 p;
+          if (tiles == 1) {
+            const uint4 v = *at;
+            p = make_int4(v.x, v.y, v.z, v.w);
+          } else {
+            p = load_pos(t);
           }
+          uint4 q;
+          q.x = t < len ? key_of(p.x, m0[u].x) : 0u;
+          q.y = t + 1u < len ? key_of(p.y, m0[u].y) : 0u;
+          q.z = t + 2u < len ? key_of(p.z, m0[u].z) : 0u;
+          q.w = t + 3u < len ? key_of(p.w, m0[u].w) : 0u;
           *at = q;
-          next_spot(sp);
         }
       }
       __syncwarp();
+      return true;
     };
     if (tiles == 1) load_tile(0);
 
@@ -258,33 +217,24 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int max_it) {
     for (int pass = 0; pass < 3 && !whole; ++pass) {
       const int sh = pass == 0 ? 20 : pass == 1 ? 10 : 0, groups = pass == 0 ? 128 : 32;
       int* hist = s_hist + (pass == 0 ? 0 : 4096 + (pass - 1) * 1024);
+      // no key is 0 in the digits above: "no token" never matches them
+      const unsigned above = pass == 0 ? 0u : thr >> (sh + 10), mask = pass == 0 ? 4095u : 1023u;
+#pragma unroll 1
       for (int k = 0; k < tiles; ++k) {
-        if (tiles > 1) load_tile(k);
-        if (warp_at(k) >= n) break;
-        if (pass == 0) {
-          for (int c = 0; c < cpl; ++c) {
-            const uint4 q = my_keys[c];
-            const unsigned first = __shfl_sync(0xffffffffu, q.x, 0) >> 20;
-            // many equal masses (zeros): one count for the warp
-            if (__all_sync(0xffffffffu, q.w != 0u && (q.x >> 20) == first && (q.y >> 20) == first &&
-                                            (q.z >> 20) == first && (q.w >> 20) == first)) {
-              if (lane == 0) atomicAdd(&hist[first], 128);
-            } else {
-              if (q.x) atomicAdd(&hist[q.x >> 20], 1);
-              if (q.y) atomicAdd(&hist[q.y >> 20], 1);
-              if (q.z) atomicAdd(&hist[q.z >> 20], 1);
-              if (q.w) atomicAdd(&hist[q.w >> 20], 1);
-            }
-          }
-        } else {
-          // no key is 0 above the digits: bit patterns of "no token" never match
-          const unsigned above = thr >> (sh + 10);
-          for (int c = 0; c < cpl; ++c) {
-            const uint4 q = my_keys[c];
-            if ((q.x >> (sh + 10)) == above) atomicAdd(&hist[(q.x >> sh) & 1023u], 1);
-            if ((q.y >> (sh + 10)) == above) atomicAdd(&hist[(q.y >> sh) & 1023u], 1);
-            if ((q.z >> (sh + 10)) == above) atomicAdd(&hist[(q.z >> sh) & 1023u], 1);
-            if ((q.w >> (sh + 10)) == above) atomicAdd(&hist[(q.w >> sh) & 1023u], 1);
+        if (tiles > 1 ? !load_tile(k) : !here) break;
+#pragma unroll 2
+        for (int c = 0; c < CPL; ++c) {
+          const uint4 q = my_keys[c];
+          auto count = [&](unsigned u) {
+            if (pass == 0 ? u != 0u : (u >> (sh + 10)) == above) atomicAdd(&hist[(u >> sh) & mask], 1);
+          };
+          // many equal masses (zeros): one count for the warp
+          const unsigned first = __shfl_sync(0xffffffffu, q.x, 0);
+          if (pass == 0 &&
+              __all_sync(0xffffffffu, ((q.x ^ first) | (q.y ^ first) | (q.z ^ first) | (q.w ^ first)) == 0u)) {
+            if (lane == 0 && first) atomicAdd(&hist[first >> 20], 128);
+          } else {
+            count(q.x); count(q.y); count(q.z); count(q.w);
           }
         }
       }
@@ -308,18 +258,19 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int max_it) {
       }
       // every warp for itself: the group, counted from the top
       const int* gs = cs > 1 ? s_gsum : s_group[pass];
-      int c[4] = {0, 0, 0, 0}, group = 0, before = 0;
-      const int per = groups / 32, top = groups - 1 - per * lane;  // this lane's first group
-#pragma unroll
-      for (int q = 0; q < 4; ++q) c[q] = q < per ? gs[top - q] : 0;
-      const int mine = (c[0] + c[1]) + (c[2] + c[3]), upto = warp_inclusive(mine, lane);
+      int group = 0, before = 0;
       {
-        const unsigned hit = __ballot_sync(0xffffffffu, upto >= want);  // not empty: want of them exist
-        const int l = __ffs(hit) - 1;
+        // lane's groups: top, top - 1 .. (four in the first pass, else one)
+        const int per = groups / 32, top = groups - 1 - per * lane;
+        int c[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c[q] = q < per ? gs[top - q] : 0;
+        const int mine = (c[0] + c[1]) + (c[2] + c[3]), upto = warp_inclusive(mine, lane);
+        const int l = __ffs(__ballot_sync(0xffffffffu, upto >= want)) - 1;  // want of them exist
         int q = 0, at = upto - mine;
 #pragma unroll
         for (int e = 0; e < 3; ++e)
-          if (q == e && e < per - 1 && at + c[e] < want) { at += c[e]; ++q; }
+          if (q == e && at + c[e] < want) { at += c[e]; ++q; }
         group = __shfl_sync(0xffffffffu, top - q, l);
         before = __shfl_sync(0xffffffffu, at, l);
       }
@@ -343,22 +294,25 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int max_it) {
     }
 
     // ---- keep words; equal keys beyond `want` leave from the highest index down
-    auto word_of = [&](auto in) {        // bit i: in(key of this lane's token i)
-      unsigned long long w = 0ull;
-      for (int c = 0; c < cpl; ++c) {
+    // bit i: this lane's token i has a key above (or at least) x
+    auto word_of = [&](unsigned x, bool equal) {
+      unsigned w = 0u;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
         const uint4 q = my_keys[c];
-        const unsigned f = (in(q.x) ? 1u : 0u) | (in(q.y) ? 2u : 0u) | (in(q.z) ? 4u : 0u) | (in(q.w) ? 8u : 0u);
-        w |= (unsigned long long)f << (4 * c);
+        const unsigned f = equal ? (q.x == x ? 1u : 0u) | (q.y == x ? 2u : 0u) | (q.z == x ? 4u : 0u) | (q.w == x ? 8u : 0u)
+                                 : (q.x >= x ? 1u : 0u) | (q.y >= x ? 2u : 0u) | (q.z >= x ? 4u : 0u) | (q.w >= x ? 8u : 0u);
+        w |= f << (4 * c);
       }
       return w;
     };
-    const unsigned thr_c = thr;
     int tie_first = 0;                   // equal keys of the CTAs before this one
     if (!whole && cs > 1) {
       int ties = 0;
+#pragma unroll 1
       for (int k = 0; k < tiles; ++k) {
-        if (tiles > 1) load_tile(k);
-        ties += __popcll(word_of([&](unsigned u) { return u == thr_c; }));
+        if (tiles > 1 ? !load_tile(k) : !here) break;
+        ties += __popc(word_of(thr, true));
       }
       ties = __reduce_add_sync(0xffffffffu, ties);
       if (lane == 0) s_wt[0][warp] = ties;
@@ -370,10 +324,12 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int max_it) {
     }
     // this lane's keep bits of tile k; `seen`: equal keys of the tiles before
     auto keep_word = [&](int k, int& seen) {
-      if (tiles > 1) load_tile(k);
-      if (whole) return word_of([&](unsigned u) { return u >= thr_c; });
-      unsigned long long tw = word_of([&](unsigned u) { return u == thr_c; });
-      const int c = __popcll(tw), upto = warp_inclusive(c, lane);
+      const bool any = tiles > 1 ? load_tile(k) : here;
+      unsigned w = any ? word_of(thr, false) : 0u;
+      if (whole) return w;
+      unsigned tw = any ? word_of(thr, true) : 0u;
+      w &= ~tw;
+      const int c = __popc(tw), upto = warp_inclusive(c, lane);
       __syncthreads();                   // the last counts are no longer read
       if (lane == 31) s_wt[0][warp] = upto;
       __syncthreads();
@@ -381,65 +337,66 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int max_it) {
       const int before = seen + __reduce_add_sync(0xffffffffu, lane < warp ? t : 0) + upto - c;
       seen += __reduce_add_sync(0xffffffffu, t);
       const int stay = min(c, max(0, want - before));
-      for (int drop = c - stay; drop > 0; --drop) tw &= ~(0x8000000000000000ull >> __clzll(tw));
-      return tw | word_of([&](unsigned u) { return u > thr_c; });
+      for (int drop = c - stay; drop > 0; --drop) tw &= ~(0x80000000u >> __clz(tw));
+      return w | tw;
     };
-    auto lane_at = [&](int k) { return warp_at(k) + (long long)lane * it; };
+    auto lane_at = [&](int k) { return warp_at(k) + (unsigned)(lane * IT); };
     // this lane's tokens before the budget (they exist: budget < n), as a mask
     auto front_word = [&](int k) {
-      const long long m = a.budget - lane_at(k);
-      return m <= 0 ? 0ull : (1ull << (int)min(m, (long long)it)) - 1ull;  // it <= 44
+      const unsigned t = lane_at(k), m = (unsigned)a.budget > t ? (unsigned)a.budget - t : 0u;
+      return m >= (unsigned)IT ? 0xffffffffu >> (32 - IT) : (1u << m) - 1u;
     };
-    unsigned long long word = 0ull;
+    unsigned word = 0u;
     int holes = 0, fills = 0, seen = tie_first;
+#pragma unroll 1
     for (int k = 0; k < tiles; ++k) {
       word = keep_word(k, seen);
-      const unsigned long long front = front_word(k);
-      holes += __popcll(~word & front);
-      fills += __popcll(word & ~front);
+      const unsigned front = front_word(k);
+      holes += __popc(~word & front);
+      fills += __popc(word & ~front);
     }
-    holes = __reduce_add_sync(0xffffffffu, holes);
-    fills = __reduce_add_sync(0xffffffffu, fills);
-    if (lane == 0) { s_wt[1][warp] = holes; s_wt[2][warp] = fills; }
-    __syncthreads();
-    const int th = s_wt[1][lane], tf = s_wt[2][lane];
-    int hole_first = 0, fill_first = 0;  // of the CTAs before this one
-    moves = __reduce_add_sync(0xffffffffu, tf);
+    // ---- lists: holes and fills of this tile in shared memory, then out
+    int hole_first = 0, fill_first = 0;  // of the CTAs (and tiles) before
     if (cs > 1) {
-      const int all_h = __reduce_add_sync(0xffffffffu, th);
-      if (tid == 0) { s_ct[2] = all_h; s_ct[3] = moves; }
+      const int h = __reduce_add_sync(0xffffffffu, holes), f = __reduce_add_sync(0xffffffffu, fills);
+      if (lane == 0) { s_wt[1][warp] = h; s_wt[2][warp] = f; }
+      __syncthreads();
+      const int all_h = __reduce_add_sync(0xffffffffu, s_wt[1][lane]);
+      const int all_f = __reduce_add_sync(0xffffffffu, s_wt[2][lane]);
+      if (tid == 0) { s_ct[2] = all_h; s_ct[3] = all_f; }
       cluster_sync();
-      const int f = lane < cs ? peer_int(&s_ct[3], lane) : 0;
-      const int h = lane < rank ? peer_int(&s_ct[2], lane) : 0;
-      moves = __reduce_add_sync(0xffffffffu, f);
-      hole_first = __reduce_add_sync(0xffffffffu, h);
-      fill_first = __reduce_add_sync(0xffffffffu, lane < rank ? f : 0);
+      const int pf = lane < cs ? peer_int(&s_ct[3], lane) : 0;
+      const int ph = lane < rank ? peer_int(&s_ct[2], lane) : 0;
+      moves = __reduce_add_sync(0xffffffffu, pf);
+      hole_first = __reduce_add_sync(0xffffffffu, ph);
+      fill_first = __reduce_add_sync(0xffffffffu, lane < rank ? pf : 0);
     }
-    if (tiles == 1) {
-      const unsigned long long front = front_word(0);
-      list_bits(~word & front, hole, hole_first + __reduce_add_sync(0xffffffffu, lane < warp ? th : 0),
-                lane_at(0), it, lane);
-      list_bits(word & ~front, fill, fill_first + __reduce_add_sync(0xffffffffu, lane < warp ? tf : 0),
-                lane_at(0), it, lane);
-    } else {
-      seen = tie_first;
-      for (int k = 0; k < tiles; ++k) {
-        word = keep_word(k, seen);
-        const unsigned long long front = front_word(k);
-        const int h = __reduce_add_sync(0xffffffffu, __popcll(~word & front));
-        const int f = __reduce_add_sync(0xffffffffu, __popcll(word & ~front));
-        __syncthreads();
-        if (lane == 0) { s_wt[1][warp] = h; s_wt[2][warp] = f; }
-        __syncthreads();
-        const int uh = s_wt[1][lane], uf = s_wt[2][lane];
-        list_bits(~word & front, hole, hole_first + __reduce_add_sync(0xffffffffu, lane < warp ? uh : 0),
-                  lane_at(k), it, lane);
-        list_bits(word & ~front, fill, fill_first + __reduce_add_sync(0xffffffffu, lane < warp ? uf : 0),
-                  lane_at(k), it, lane);
-        hole_first += __reduce_add_sync(0xffffffffu, uh);
-        fill_first += __reduce_add_sync(0xffffffffu, uf);
-      }
+    seen = tie_first;
+    int* list = reinterpret_cast<int*>(s_key);
+#pragma unroll 1
+    for (int k = 0; k < tiles; ++k) {
+      if (tiles > 1) word = keep_word(k, seen);
+      const unsigned front = front_word(k);
+      unsigned hw = ~word & front, fw = word & ~front;
+      const int both = __popc(hw) | __popc(fw) << 16, upto = warp_inclusive(both, lane);
+      __syncthreads();                   // keys and the last counts are no longer read
+      if (lane == 31) s_wt[1][warp] = upto;
+      __syncthreads();
+      const int t = s_wt[1][lane];       // at most 2^15 of each: no carry
+      const unsigned before = (unsigned)(__reduce_add_sync(0xffffffffu, lane < warp ? (unsigned)t : 0u) + upto - both);
+      const unsigned all = __reduce_add_sync(0xffffffffu, (unsigned)t);
+      const int nh = all & 0xffffu, nf = all >> 16;
+      const int t0 = (int)lane_at(k);
+      for (int at = before & 0xffffu; hw; hw &= hw - 1) list[at++] = t0 + __ffs(hw) - 1;
+      for (int at = nh + (before >> 16); fw; fw &= fw - 1) list[at++] = t0 + __ffs(fw) - 1;
+      __syncthreads();
+      for (int i = tid; i < nh; i += kEvThreads) hole[hole_first + i] = list[i];
+      for (int i = tid; i < nf; i += kEvThreads) fill[fill_first + i] = list[nh + i];
+      hole_first += nh;
+      fill_first += nf;
+      if (tiles > 1) __syncthreads();
     }
+    if (cs == 1) moves = fill_first;
     if (cs > 1) cluster_sync();          // no CTA leaves while its counts are read
   }
   for (int i = moves + rank * kEvThreads + tid; i < a.max_move; i += cs * kEvThreads)
@@ -516,14 +473,15 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, int groups, long lon
   }
 }
 
-template <bool VEC>
-cudaError_t run_evict(const EvictArgs& a, int cs, int it, cudaStream_t st) {
-  cudaError_t e = allow_smem<evict_select_kernel<VEC>>((kMaxIt / 4 | 1) * 16 * kEvThreads);
+template <int CPL, bool VEC>
+cudaError_t run_evict(const EvictArgs& a, int cs, int tiles, cudaStream_t st) {
+  constexpr int kSmem = (CPL | 1) * 16 * kEvThreads;
+  cudaError_t e = allow_smem<evict_select_kernel<CPL, VEC>>(kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.s.batch * a.n_mass) * cs);
   cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = (size_t)(it / 4 | 1) * 16 * kEvThreads;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -533,25 +491,32 @@ cudaError_t run_evict(const EvictArgs& a, int cs, int it, cudaStream_t st) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<VEC>, a, cs, it);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<CPL, VEC>, a, cs, tiles);
+}
+
+template <bool VEC>
+cudaError_t run_evict(const EvictArgs& a, int cs, long long chunks, cudaStream_t st) {
+  if (chunks <= 1) return run_evict<1, VEC>(a, cs, 1, st);
+  if (chunks <= 2) return run_evict<2, VEC>(a, cs, 1, st);
+  if (chunks <= 4) return run_evict<4, VEC>(a, cs, 1, st);
+  return run_evict<kMaxChunks, VEC>(a, cs, (int)((chunks + kMaxChunks - 1) / kMaxChunks), st);
 }
 
 }  // namespace
 
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st) {
-  // As many CTAs a row as keep one per SM, at least 1024 tokens each; longer
+  // As many CTAs a row as keep one per SM, at least one chunk a thread; longer
   // rows take more, up to the cluster's eight.
   const long long rows = (long long)a.s.batch * a.n_mass, L = a.s.L_ctx;
   const int sms = tc_sm_count();
   int cs = 1;
-  while (cs < kMaxCluster && ((rows * cs * 2 <= sms && L > (long long)cs * kEvThreads) ||
-                              L > (long long)cs * kMaxIt * kEvThreads))
+  while (cs < kMaxCluster && ((rows * cs * 2 <= sms && L > 4ll * cs * kEvThreads) ||
+                              L > 4ll * cs * kMaxChunks * kEvThreads))
     cs *= 2;
-  const long long per = (L + 4ll * cs * kEvThreads - 1) / (4ll * cs * kEvThreads) * 4;
-  const int it = (int)(per < kMaxIt ? (per > 0 ? per : 4) : kMaxIt);
+  const long long chunks = (L + 4ll * cs * kEvThreads - 1) / (4ll * cs * kEvThreads);
   const bool vec = L % 4 == 0 && (reinterpret_cast<uintptr_t>(a.tok_mass) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(a.tok_pos) & 15) == 0;
-  return vec ? run_evict<true>(a, cs, it, st) : run_evict<false>(a, cs, it, st);
+  return vec ? run_evict<true>(a, cs, chunks, st) : run_evict<false>(a, cs, chunks, st);
 }
 
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {
