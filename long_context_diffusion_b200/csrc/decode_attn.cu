@@ -32,9 +32,15 @@
 // fp32: the same walk on the CUDA cores (exact products, fp32 sums): lane =
 // (key, quarter of d) for S, lane = four columns for O.
 //
-// Masses.  The main kernel leaves the logits (base-2 units) in the workspace;
-// the join kernel's other CTAs turn them into weights with the joined sums and
-// add them over the heads, in head order.
+// Weights.  With c = scale log2 e and a maximum m of the dot products x, the
+// reference is M = m c rounded once, and p = 2^(x c - M) in one fused
+// operation: its argument is rounded at its own size, not at that of x c (a
+// sink's logit of 35 would cost 1e-6 of every weight beside it).  Everything
+// that is joined is relative to these M.
+//
+// Masses.  The main kernel leaves the dot products in the workspace; the join
+// kernel's other CTAs turn them into weights with the joined maxima and sums
+// and add them over the heads, in head order.
 #include <atomic>
 
 #include "common.cuh"
@@ -73,9 +79,9 @@ constexpr int kItemCost = 3;
 struct DecodeWs {
   int* runs;         // [batch][items][2]: first and last run of each item
   float* po;         // [2 kMaxCtas][RB][d] unnormalised partial outputs
-  float2* pml;       // [2 kMaxCtas][RB] (maximum, sum), base-2 units
-  float* lse2;       // [batch][H] of the items finished in one run, base-2
-  float* logit;      // [batch][H][Lp] base-2 (with masses)
+  float2* pml;       // [2 kMaxCtas][RB] (reference, sum)
+  float2* norm;      // [batch][H] (reference, 1 / sum) of the items finished in one run
+  float* logit;      // [batch][H][Lp] dot products (with masses)
   int Lp;
 };
 
@@ -89,7 +95,7 @@ size_t carve(const Shape& s, bool mass, void* ws, DecodeWs* w) {
   d.runs = reinterpret_cast<int*>(take((size_t)s.batch * items_per_seq(s) * 8));
   d.po = reinterpret_cast<float*>(take((size_t)2 * kMaxCtas * rb * s.d * 4));
   d.pml = reinterpret_cast<float2*>(take((size_t)2 * kMaxCtas * rb * 8));
-  d.lse2 = reinterpret_cast<float*>(take((size_t)s.batch * s.H * 4));
+  d.norm = reinterpret_cast<float2*>(take((size_t)s.batch * s.H * 8));
   d.logit = reinterpret_cast<float*>(take(mass ? (size_t)s.batch * s.H * d.Lp * 4 : 0));
   if (w) *w = d;
   return at;
@@ -253,8 +259,7 @@ struct StateTc {
     for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float v = s[j >> 1][2 * r + (j & 1)] * c2;
-        x[r][j] = !part || ok[j >> 1][j & 1] ? v : -INFINITY;
+        x[r][j] = !part || ok[j >> 1][j & 1] ? s[j >> 1][2 * r + (j & 1)] : -INFINITY;
       }
     if (logit) {
 #pragma unroll
@@ -280,7 +285,7 @@ struct StateTc {
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const float f = top[r] == -INFINITY ? 1.0f : ex2_approx(m[r] - top[r]);
+        const float f = top[r] == -INFINITY ? 1.0f : ex2_approx(__fmul_rn(m[r], c2) - __fmul_rn(top[r], c2));
         m[r] = top[r];
         l[r] *= f;
 #pragma unroll
@@ -293,10 +298,10 @@ struct StateTc {
     uint32_t hi[NR][2], lo[NR][2];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const float base = m[r] == -INFINITY ? 0.0f : m[r];
+      const float M = m[r] == -INFINITY ? 0.0f : __fmul_rn(m[r], c2);
       float p[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = ex2_approx(x[r][j] - base);
+      for (int j = 0; j < 4; ++j) p[j] = ex2_approx(fmaf(x[r][j], c2, -M));
       l[r] += (p[0] + p[1]) + (p[2] + p[3]);
       split_bf16(p[0], p[1], hi[r][0], lo[r][0]);
       split_bf16(p[2], p[3], hi[r][1], lo[r][1]);
@@ -338,10 +343,10 @@ struct StateTc {
       for (int i = 0; i < D / 8; ++i) { o[i][0] += o[i][2]; o[i][1] += o[i][3]; }
     }
   }
-  __device__ __forceinline__ void put_ml(float2* ml, int lane) const {
+  __device__ __forceinline__ void put_ml(float2* ml, int lane, float c2) const {
     if ((lane & 3) == 0) {
 #pragma unroll
-      for (int r = 0; r < NR; ++r) ml[lane / 4 + 8 * r] = make_float2(m[r], l[r]);
+      for (int r = 0; r < NR; ++r) ml[lane / 4 + 8 * r] = make_float2(__fmul_rn(m[r], c2), l[r]);
     }
   }
   __device__ __forceinline__ void scale(const float* f, int lane) {  // f: per row, shared memory
@@ -421,7 +426,7 @@ struct StateF32 {
     for (int r = 0; r < RB; ++r) {
       x[r] += __shfl_xor_sync(0xffffffffu, x[r], 8);
       x[r] += __shfl_xor_sync(0xffffffffu, x[r], 16);
-      x[r] = ok ? x[r] * c2 : -INFINITY;
+      x[r] = ok ? x[r] : -INFINITY;
       if (logit && dq == 0 && r < n_rows) logit[(size_t)r * Lp + key] = x[r];
       float t = x[r];
 #pragma unroll
@@ -432,7 +437,7 @@ struct StateF32 {
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
-        const float f = top[r] == -INFINITY ? 1.0f : ex2_approx(m[r] - top[r]);
+        const float f = top[r] == -INFINITY ? 1.0f : ex2_approx(__fmul_rn(m[r], c2) - __fmul_rn(top[r], c2));
         m[r] = top[r];
         l[r] *= f;
 #pragma unroll
@@ -442,7 +447,7 @@ struct StateF32 {
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
-      const float p = ex2_approx(x[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
+      const float p = ex2_approx(fmaf(x[r], c2, m[r] == -INFINITY ? 0.0f : -__fmul_rn(m[r], c2)));
       l[r] += p;
       if (dq == (r & 3)) sp[r * 8 + kk] = p;
     }
@@ -474,10 +479,10 @@ struct StateF32 {
       }
     }
   }
-  __device__ __forceinline__ void put_ml(float2* ml, int lane) const {
+  __device__ __forceinline__ void put_ml(float2* ml, int lane, float c2) const {
     if (lane == 0) {
 #pragma unroll
-      for (int r = 0; r < RB; ++r) ml[r] = make_float2(m[r], l[r]);
+      for (int r = 0; r < RB; ++r) ml[r] = make_float2(__fmul_rn(m[r], c2), l[r]);
     }
   }
   __device__ __forceinline__ void scale(const float* f, int) {
@@ -512,6 +517,11 @@ struct StateF32 {
     }
   }
 };
+
+// Natural log-sum of a row with reference M and sum L (L = 0: no key).
+__device__ __forceinline__ float lse_of(float M, float L) {
+  return L > 0.0f ? (M + log2f(L)) * kLn2 : (L != L ? L : -INFINITY);
+}
 
 __device__ __forceinline__ void store2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 __device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v) {
@@ -678,7 +688,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     }
     // segment end: the four warps' states, added in warp order
     st8.finish(lane);
-    st8.put_ml(s_ml + warp * RB, lane);
+    st8.put_ml(s_ml + warp * RB, lane, c2);
     named_bar_sync(1, kWarps * 32);
     if (lane < RB) {
       float M = -INFINITY;
@@ -719,9 +729,8 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
       float inv = L > 0.0f ? 1.0f / L : 0.0f;
       if (L != L) inv = L;
       if (lane < n_rows) {
-        const float lse2 = L > 0.0f ? M + log2f(L) : (L != L ? L : -INFINITY);
-        ws.lse2[row0 + lane] = lse2;
-        if (a.lse) a.lse[row0 + lane] = lse2 * kLn2;
+        ws.norm[row0 + lane] = make_float2(L == 0.0f ? INFINITY : M, inv);  // no key: weights 2^-inf
+        if (a.lse) a.lse[row0 + lane] = lse_of(M, L);
       }
       T* O = reinterpret_cast<T*>(a.O) + row0 * D;
       __syncwarp();
@@ -754,11 +763,11 @@ __device__ __forceinline__ Parts parts_of(const DecodeArgs& a, const DecodeWs& w
   return Parts{runs.x, runs.y - runs.x + 1, r % rb};
 }
 
-// Base-2 log-sum of one query row over its runs, by one warp.  A row finished
-// by its run has it in the workspace.
-__device__ __forceinline__ float row_lse2(const DecodeArgs& a, const DecodeWs& ws, const Parts& p, size_t row,
-                                          int rb, int lane) {
-  if (p.n == 1) return ws.lse2[row];
+// Reference and inverse sum of one query row over its runs, by one warp.  A
+// row finished by its run has them in the workspace.
+__device__ __forceinline__ float2 row_norm(const DecodeArgs& a, const DecodeWs& ws, const Parts& p, size_t row,
+                                           int rb, int lane) {
+  if (p.n == 1) return ws.norm[row];
   float M = -INFINITY, L = 0.0f;
 #pragma unroll 3
   for (int i = lane; i < p.n; i += 32) {
@@ -771,7 +780,7 @@ __device__ __forceinline__ float row_lse2(const DecodeArgs& a, const DecodeWs& w
   }
   const float top = warp_max(M);
   L = warp_sum(top == -INFINITY ? L : L * ex2_approx(M - top));
-  return top + log2f(L);
+  return L == 0.0f ? make_float2(INFINITY, 0.0f) : make_float2(top, 1.0f / L);
 }
 
 // CTA `id` of the masses: one of `chunks` of a decision row.  A thread has
@@ -780,7 +789,7 @@ template <int QR>
 __device__ __forceinline__ void add_masses(const DecodeArgs& a, const DecodeWs& ws, int rb, int id,
                                            int chunks) {
   constexpr int NW = kJoinThreads / 32, TJ = 8 / QR;
-  __shared__ float s_lse[64];            // 64 rows at a time
+  __shared__ float2 s_norm[64];          // 64 rows at a time
   const Shape& s = a.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bm = id / chunks, b = bm / a.n_mass, m = bm % a.n_mass;
@@ -789,6 +798,7 @@ __device__ __forceinline__ void add_masses(const DecodeArgs& a, const DecodeWs& 
   const int n = seq_len(a, b);
   if (first >= n) return;
   float* mass = a.tok_mass + ((size_t)b * a.n_mass + m) * s.L_ctx;
+  const float c2 = (float)(s.scale * 1.4426950408889634);
   pdl_wait();
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += 64) {
@@ -816,17 +826,18 @@ __device__ __forceinline__ void add_masses(const DecodeArgs& a, const DecodeWs& 
           sums = true;
           __syncthreads();
           for (int r = warp; r < nr; r += NW) {
-            const float lse = row_lse2(a, ws, parts_of(a, ws, b, h0 + r0 + r, rb),
-                                       (size_t)b * s.H + h0 + r0 + r, rb, lane);
-            if (lane == 0) s_lse[r] = lse == -INFINITY ? INFINITY : lse;  // no weight at all: 2^-inf
+            const float2 norm = row_norm(a, ws, parts_of(a, ws, b, h0 + r0 + r, rb),
+                                         (size_t)b * s.H + h0 + r0 + r, rb, lane);
+            if (lane == 0) s_norm[r] = norm;
           }
           __syncthreads();
         }
 #pragma unroll
         for (int q = 0; q < QR; ++q) {
-          const float l2 = q0 + q < nr ? s_lse[q0 + q] : INFINITY;
+          if (q0 + q >= nr) continue;
+          const float2 norm = s_norm[q0 + q];
 #pragma unroll
-          for (int j = 0; j < TJ; ++j) sum[j] += ex2_approx(v[q][j] - l2);
+          for (int j = 0; j < TJ; ++j) sum[j] = fmaf(ex2_approx(fmaf(v[q][j], c2, -norm.x)), norm.y, sum[j]);
         }
       }
 #pragma unroll
@@ -922,8 +933,7 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
       T* dst = reinterpret_cast<T*>(a.O) + (size_t)row * D + 4 * tid;
       store2(dst, make_float2(o.x * inv, o.y * inv));
       store2(dst + 2, make_float2(o.z * inv, o.w * inv));
-      if (tid == 0 && a.lse)
-        a.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : (L != L ? L : -INFINITY);
+      if (tid == 0 && a.lse) a.lse[row] = lse_of(M, L);
     }
     return;
   }
