@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI declared in include/dl.h.
+"""Binding of the C ABI declared in include/dl.h: ctypes, and a small CPython
+extension for the calls that run for microseconds.
 
 Argument marshalling only: each function has the C entry point's name and
 arguments, takes torch tensors for the device buffers (their data pointers
@@ -9,6 +10,8 @@ A failing call raises DLError with the library's message.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
@@ -260,53 +263,38 @@ def dl_block_scores_noalloc(desc, Q_dec, q_idx, q_cnt, Kbar, n_units, score, str
 
 
 # ---- one token at a time over the same cache (dl.h, c1-c4) ----
+# Marshalled by the CPython extension of csrc/bind_calls.cpp, which also checks
+# every buffer's type, size, contiguity and device (ValueError).
 
-# The current stream of a device as its raw handle: a tenth of the cost of
-# building a torch.cuda.Stream, which counts in calls of a few microseconds.
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _device_of(name: str, t: torch.Tensor) -> int:
-    """The device a call launches on: that of its buffers, which must be the
-    current one."""
-    dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"{name}: buffers must be on the current CUDA device, got {t.device}")
-    return dev
+CALLS_PATH = os.path.join(_PKG, "lib", "_calls.so")
 
 
-def _buf(t, dtype, n: int, dev: int, what: str):
-    """Data pointer of a call's buffer (None: NULL) of n elements of dtype on
-    device dev."""
-    if t is None:
+def _load_calls():
+    if not os.path.exists(CALLS_PATH):
+        raise ImportError(
+            f"{CALLS_PATH} is missing: build it with `python -m long_context_diffusion_b200.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_calls", CALLS_PATH)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+    loader.exec_module(mod)
+    return mod
+
+
+def _bind_calls(of):
+    """Points the extension at the entry points of the loaded library `of`."""
+    _calls.bind(torch.Tensor, torch.cuda.current_device,
+                *(ctypes.cast(getattr(of, n), ctypes.c_void_p).value for n in
+                  ("dl_qk_norm_rope", "dl_decode_attn", "dl_evict_select", "dl_cache_compact")))
+
+
+_calls = _load_calls()
+_bind_calls(lib)
+
+
+def _raw(stream):
+    """A stream argument as the extension takes it: None or a raw handle."""
+    if stream is None:
         return None
-    if t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements on the current CUDA "
-                     f"device ({dev}), got {t.dtype} {tuple(t.shape)} on {t.device}")
-
-
-def _stream(stream, dev: int):
-    return _current_raw_stream(dev) if stream is None else _s(stream)
-
-
-_I32, _F32 = torch.int32, torch.float32
-
-
-def _dtype_of(desc):
-    return torch.bfloat16 if desc.dtype == DL_BF16 else torch.float32
-
-
-def _mass_rows(name, *arrays):
-    """Rows per sequence of the per-token arrays [batch][n_mass][...]."""
-    for t in arrays:
-        if t is not None:
-            if t.dim() != 3:
-                raise ValueError(f"{name}: per-token arrays are [batch][n_mass][...], got "
-                                 f"{tuple(t.shape)}")
-            return t.shape[1]
-    return 1
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def dl_qk_norm_rope(desc, qkv, pos, q_weight, k_weight, eps, inv_freq, Q_out, K_out=None,
@@ -316,90 +304,36 @@ def dl_qk_norm_rope(desc, qkv, pos, q_weight, k_weight, eps, inv_freq, Q_out, K_
     further apart (unit stride inside a token, equal steps between tokens).
     inv_freq None: no rotation.  Outputs: Q_out, and K_out/V_out and/or the
     cache (start, page_table, K_pool, V_pool, with end, tok_pos, tok_mass)."""
-    B, H, H_kv, d = desc.batch, desc.H, desc.H_kv, desc.d
-    dt, dev = _dtype_of(desc), _device_of("dl_qk_norm_rope", qkv)
-    width = (H + 2 * H_kv) * d
-    if qkv.dim() != 3 or qkv.dtype is not dt:
-        raise ValueError(f"dl_qk_norm_rope: qkv must be a [batch][n_tok][...] {dt} tensor, got "
-                         f"{qkv.dtype} {tuple(qkv.shape)}")
-    (b, n, w), (s0, stride, s2) = qkv.shape, qkv.stride()
-    if n == 1:
-        stride = s0 if B > 1 else max(stride, w)
-    if b != B or s2 != 1 or w < width or stride < w or (B > 1 and n > 1 and s0 != n * stride):
-        raise ValueError(f"dl_qk_norm_rope: qkv must hold {B} sequences whose token rows have "
-                         f"(H + 2 H_kv) d = {width} values with unit stride and equal steps between "
-                         f"tokens, got shape {tuple(qkv.shape)} strides {qkv.stride()}")
-    rows = B * n * d
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    n_mass = start_p = table_p = kp = vp = end_p = tp = tm = None
-    if start is not None:
-        pool = desc.n_slots * H_kv * desc.page * d
-        n_mass = _mass_rows("dl_qk_norm_rope", tok_pos, tok_mass)
-        book = B * n_mass * desc.L_ctx
-        start_p = _buf(start, _I32, B, dev, "start")
-        table_p = _buf(page_table, _I32, B * desc.n_pages, dev, "page_table")
-        kp, vp = _buf(K_pool, dt, pool, dev, "K_pool"), _buf(V_pool, dt, pool, dev, "V_pool")
-        end_p = _buf(end, _I32, B, dev, "end")
-        tp, tm = _buf(tok_pos, _I32, book, dev, "tok_pos"), _buf(tok_mass, _F32, book, dev, "tok_mass")
-    elif not (page_table is K_pool is V_pool is end is tok_pos is tok_mass is None):
-        raise ValueError("dl_qk_norm_rope: page_table, pools, end, tok_pos and tok_mass need start")
-    _check(lib.dl_qk_norm_rope(
-        ctypes.byref(desc), qkv.data_ptr(), stride, n, _buf(pos, _I32, B * n, dev, "pos"),
-        _buf(q_weight, dt, d, dev, "q_weight"), _buf(k_weight, dt, d, dev, "k_weight"), eps,
-        _buf(inv_freq, _F32, rot // 2, dev, "inv_freq"), rot, interleaved,
-        _buf(Q_out, dt, rows * H, dev, "Q_out"), _buf(K_out, dt, rows * H_kv, dev, "K_out"),
-        _buf(V_out, dt, rows * H_kv, dev, "V_out"), start_p, table_p, kp, vp, end_p, tp, tm,
-        n_mass or 1, _stream(stream, dev)))
+    st = _calls.qk_norm_rope(desc, qkv, pos, q_weight, k_weight, eps, inv_freq, Q_out, K_out, V_out,
+                             start, page_table, K_pool, V_pool, end, tok_pos, tok_mass, interleaved,
+                             stream if stream is None else _raw(stream))
+    if st:
+        _check(st)
 
 
 def dl_decode_attn(desc, Q, K_pool, V_pool, page_table, ctx_len, O, lse, ws, tok_mass=None,
                    decay=1.0, stream=None):
     """tok_mass [batch][1 or H_kv][L_ctx], accumulated in place (or None)."""
-    B, H, d = desc.batch, desc.H, desc.d
-    dt, dev = _dtype_of(desc), _device_of("dl_decode_attn", Q)
-    pool, n_mass, mass = desc.n_slots * desc.H_kv * desc.page * d, 1, None
-    if tok_mass is not None:
-        n_mass = _mass_rows("dl_decode_attn", tok_mass)
-        mass = _buf(tok_mass, _F32, B * n_mass * desc.L_ctx, dev, "tok_mass")
-    _check(lib.dl_decode_attn(
-        ctypes.byref(desc), _buf(Q, dt, B * H * d, dev, "Q"), _buf(K_pool, dt, pool, dev, "K_pool"),
-        _buf(V_pool, dt, pool, dev, "V_pool"),
-        _buf(page_table, _I32, B * desc.n_pages, dev, "page_table"),
-        _buf(ctx_len, _I32, B, dev, "ctx_len"), _buf(O, dt, B * H * d, dev, "O"),
-        _buf(lse, _F32, B * H, dev, "lse"), mass, n_mass, decay,
-        _buf(ws, ws.dtype, ws.numel(), dev, "ws"), ws.numel() * ws.element_size(),
-        _stream(stream, dev)))
+    st = _calls.decode_attn(desc, Q, K_pool, V_pool, page_table, ctx_len, O, lse, ws, tok_mass,
+                            decay, stream if stream is None else _raw(stream))
+    if st:
+        _check(st)
 
 
 def dl_evict_select(desc, tok_mass, tok_pos, ctx_len, budget, n_first, n_recent, hole_idx,
                     fill_idx, move_cnt, new_len, stream=None):
     """hole_idx, fill_idx [batch][n_mass][max_move]; tok_pos may be None (the
     index is the position)."""
-    B, dev = desc.batch, _device_of("dl_evict_select", tok_mass)
-    n_mass = _mass_rows("dl_evict_select", tok_mass)
-    max_move = 0 if hole_idx is None else hole_idx.shape[-1]
-    book, moves = B * n_mass * desc.L_ctx, B * n_mass * max_move
-    _check(lib.dl_evict_select(
-        ctypes.byref(desc), _buf(tok_mass, _F32, book, dev, "tok_mass"),
-        _buf(tok_pos, _I32, book, dev, "tok_pos"), n_mass, _buf(ctx_len, _I32, B, dev, "ctx_len"),
-        budget, n_first, n_recent, _buf(hole_idx, _I32, moves, dev, "hole_idx"),
-        _buf(fill_idx, _I32, moves, dev, "fill_idx"), max_move,
-        _buf(move_cnt, _I32, B * n_mass, dev, "move_cnt"), _buf(new_len, _I32, B, dev, "new_len"),
-        _stream(stream, dev)))
+    st = _calls.evict_select(desc, tok_mass, tok_pos, ctx_len, budget, n_first, n_recent, hole_idx,
+                             fill_idx, move_cnt, new_len, stream if stream is None else _raw(stream))
+    if st:
+        _check(st)
 
 
 def dl_cache_compact(desc, hole_idx, fill_idx, move_cnt, page_table, K_pool, V_pool, tok_pos=None,
                      tok_mass=None, stream=None):
     """The moves of dl_evict_select's lists ([batch][n_mass][max_move])."""
-    B, dev, dt = desc.batch, _device_of("dl_cache_compact", K_pool), _dtype_of(desc)
-    n_mass = _mass_rows("dl_cache_compact", hole_idx)
-    max_move, pool = hole_idx.shape[-1], desc.n_slots * desc.H_kv * desc.page * desc.d
-    book, moves = B * n_mass * desc.L_ctx, B * n_mass * max_move
-    _check(lib.dl_cache_compact(
-        ctypes.byref(desc), _buf(hole_idx, _I32, moves, dev, "hole_idx"),
-        _buf(fill_idx, _I32, moves, dev, "fill_idx"),
-        _buf(move_cnt, _I32, B * n_mass, dev, "move_cnt"), max_move, n_mass,
-        _buf(page_table, _I32, B * desc.n_pages, dev, "page_table"),
-        _buf(K_pool, dt, pool, dev, "K_pool"), _buf(V_pool, dt, pool, dev, "V_pool"),
-        _buf(tok_pos, _I32, book, dev, "tok_pos"), _buf(tok_mass, _F32, book, dev, "tok_mass"),
-        _stream(stream, dev)))
+    st = _calls.cache_compact(desc, hole_idx, fill_idx, move_cnt, page_table, K_pool, V_pool, tok_pos,
+                              tok_mass, stream if stream is None else _raw(stream))
+    if st:
+        _check(st)

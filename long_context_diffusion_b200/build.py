@@ -1,4 +1,5 @@
-"""Builds the C-ABI shared library (libdlsparse.so) in-tree for sm_100a.
+"""Builds the C-ABI shared library (libdlsparse.so) in-tree for sm_100a, and
+the CPython binding of its token-by-token calls (_calls.so).
 
     python long_context_diffusion_b200/build.py        (or __graft_entry__.build())
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(LIBDIR, "libdlsparse.so")
+CALLS = os.path.join(LIBDIR, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -38,6 +41,31 @@ def _newest_header() -> float:
     hs = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
     return max((os.path.getmtime(h) for h in hs), default=0.0)
+
+
+def _torch_include() -> str:
+    """torch's header folder (for its dlpack.h), without importing torch."""
+    import importlib.util
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found")
+    return os.path.join(spec.submodule_search_locations[0], "include")
+
+
+def build_calls() -> str:
+    """The CPython extension of csrc/bind_calls.cpp."""
+    src, hdr = os.path.join(CSRC, "bind_calls.cpp"), os.path.join(ROOT, "include", "dl.h")
+    if os.path.exists(CALLS) and os.path.getmtime(CALLS) >= max(os.path.getmtime(src),
+                                                                os.path.getmtime(hdr)):
+        return CALLS
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I",
+           os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"], "-I",
+           _torch_include(), src, "-o", CALLS + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(CALLS + ".tmp", CALLS)
+    return CALLS
 
 
 def build(verbose: bool = False, extra: list | None = None) -> str:
@@ -74,6 +102,7 @@ def build(verbose: bool = False, extra: list | None = None) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(LIB + ".tmp", LIB)
+    build_calls()
     return LIB
 
 
