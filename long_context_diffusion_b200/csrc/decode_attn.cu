@@ -16,6 +16,11 @@
 // its runs leaves a partial (maximum, sum, unnormalised output) in the
 // workspace, and the join kernel adds them in run order.
 //
+// Small problems (few tiles for every CTA, all CTAs resident at once) take the
+// items whole instead: a cluster of up to 8 CTAs shares an item's tiles, joins
+// through its shared memory and adds the masses itself, so the join kernel,
+// half of such a call's time, is not needed.
+//
 // Roles.  Warp 4 copies pages into a ring of shared-memory stages by TMA
 // (128-byte swizzle) through the page table, running ahead across segments.
 // Warps 0-3 take a quarter of each tile's keys each, with a running maximum
@@ -43,6 +48,7 @@
 // and add them over the heads, in head order.
 #include <atomic>
 
+#include "cluster.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -60,11 +66,19 @@ constexpr int kThreads = (kWarps + 1) * 32;     // + the copying warp
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 148 * kCtasPerSm;      // partial slots are sized for this many
 constexpr int kJoinThreads = 256;
+constexpr int kMaxCluster = 8;
+// Most tiles of a cluster CTA: 4, or 16 when clusters fill three quarters of the
+// GPU and equal runs would be as long (bf16, d 128, clusters against runs: 8
+// items of 4 tiles a CTA 10.3 to 12.3 us, of 8 tiles 14.4 to 12.3; 32 items of 8
+// tiles 18.3 to 21.4, of 16 tiles 28.1 to 31.2).
+constexpr int kClusterTiles = 4, kClusterTilesFull = 16;
 constexpr float kLn2 = 0.69314718055994531f;
 
-// Query heads per item block: 8, or 16 for bf16 groups of more than 8.
+// Query heads per item block: 8; 16 for bf16 groups of more than 8; 2 for fp32
+// groups of at most 2 (on the CUDA cores empty rows cost as much as others).
 __host__ __device__ inline int rows_per_block(const Shape& s) {
-  return s.dtype == DL_BF16 && s.G > 8 ? 16 : 8;
+  if (s.dtype == DL_BF16) return s.G > 8 ? 16 : 8;
+  return s.G > 2 ? 8 : 2;
 }
 __host__ __device__ inline int items_per_seq(const Shape& s) {
   const int rb = rows_per_block(s);
@@ -150,6 +164,18 @@ struct Walk {
       if (s->t1 > s->t0) return true;  // else the run ends inside the item's extra count
     }
     return false;
+  }
+};
+
+// A cluster CTA's only segment (possibly without tiles).
+struct Single {
+  Segment seg;
+  bool done;
+  __device__ bool next(Segment* s) {
+    if (done) return false;
+    done = true;
+    *s = seg;
+    return true;
   }
 };
 
@@ -528,10 +554,136 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v) {
   *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.x, v.y);
 }
 
+// The end of a cluster CTA, by all its threads: the cluster's states are joined
+// (each CTA some of the columns), then each CTA adds its own tokens' masses if
+// no other item adds to them (`own_mass`); else the join kernel does, with the
+// norms left here.
 template <typename T, int D, int RB>
+__device__ __forceinline__ void cluster_finish(const DecodeArgs& a, const DecodeWs& ws, char* sm, const Segment& seg,
+                                               int cs, bool own_mass) {
+  using C = Cfg<T, D, RB>;
+  __shared__ float2 s_norm[RB];          // joined (reference, 1 / sum) of each row
+  const Shape& s = a.s;
+  const float2* s_ml = reinterpret_cast<const float2*>(sm + C::ML_OFF);
+  const float2* s_o = reinterpret_cast<const float2*>(sm + C::O_OFF);
+  const int tid = threadIdx.x, rank = cs > 1 ? cluster_rank() : 0;
+  const int nrb = (s.G + RB - 1) / RB, g = seg.item / nrb, r0 = (seg.item % nrb) * RB, n_rows = min(RB, s.G - r0);
+  const size_t row0 = (size_t)seg.b * s.H + g * s.G + r0;
+  if (cs > 1) cluster_sync(); else __syncthreads();
+  auto state = [&](const float2* p, int k) { return cs > 1 ? peer_float2(p, k) : *p; };
+  const int cols = D / 2 / cs;           // pairs of columns of this CTA
+  for (int e = tid; e < n_rows * cols; e += kThreads) {
+    const int r = e / cols, col = rank * cols + e % cols;
+    float2 ml[kMaxCluster], v[kMaxCluster];
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) {
+      ml[k] = k < cs ? state(s_ml + r, k) : make_float2(-INFINITY, 0.0f);
+      v[k] = k < cs ? state(s_o + r * (D / 2) + col, k) : make_float2(0.0f, 0.0f);
+    }
+    float M = -INFINITY, L = 0.0f;
+    float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, ml[k].x);
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) {
+      const float f = ml[k].x == -INFINITY ? 0.0f : ex2_approx(ml[k].x - M);
+      L = fmaf(ml[k].y, f, L);
+      o.x = fmaf(v[k].x, f, o.x);
+      o.y = fmaf(v[k].y, f, o.y);
+    }
+    float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    if (L != L) inv = L;
+    store2(reinterpret_cast<T*>(a.O) + (row0 + r) * D + 2 * col, make_float2(o.x * inv, o.y * inv));
+    if (col == rank * cols) {
+      s_norm[r] = make_float2(L == 0.0f ? INFINITY : M, inv);  // no key: weights 2^-inf
+      if (rank == 0) {
+        if (a.lse) a.lse[row0 + r] = lse_of(M, L);
+        if (!own_mass) {
+          ws.norm[row0 + r] = s_norm[r];
+          if (r == 0) reinterpret_cast<int2*>(ws.runs)[(size_t)seg.b * s.H_kv * nrb + seg.item] = make_int2(0, 0);
+        }
+      }
+    }
+  }
+  if (cs > 1) cluster_sync(); else __syncthreads();  // no CTA leaves while its state is read
+  if (!a.tok_mass || !own_mass) return;
+  const float c2 = (float)(s.scale * 1.4426950408889634);
+  float* mass = a.tok_mass + ((size_t)seg.b * s.H_kv + g) * s.L_ctx;
+  const float* x = ws.logit + row0 * ws.Lp;
+  for (int t = seg.t0 * C::KT + tid; t < min(seg.len, seg.t1 * C::KT); t += kThreads) {
+    const float old = a.decay != 0.0f ? mass[t] : 0.0f;
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int r = 0; r < n_rows; ++r)
+      sum = fmaf(ex2_approx(fmaf(x[(size_t)r * ws.Lp + t], c2, -s_norm[r].x)), s_norm[r].y, sum);
+    mass[t] = a.decay == 0.0f ? sum : fmaf(a.decay, old, sum);
+  }
+}
+
+// The run of CTA c of `grid`: its part of the counted tiles of all sequences.
+// Every warp finds it for itself: a lane counts `per` sequences; the one whose
+// count passes the run's first tile has the place.
+__device__ __forceinline__ Walk find_run(const DecodeArgs& a, int c, int grid, int ips, int kt, bool report) {
+  const Shape& s = a.s;
+  const int lane = threadIdx.x & 31;
+  const int per = (s.batch + 31) / 32, b0 = min(s.batch, lane * per), b1 = min(s.batch, b0 + per);
+  long long mine = 0;
+  int n0 = 0;                            // length of sequence b0
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) {
+    const int n = a.ctx_len[b];
+    const bool ok = n >= 0 && n <= s.L_ctx;
+    if (!ok && report) flag_error(a.err, ERR_BAD_INDEX);
+    const int len = ok ? n : 0;
+    if (b == b0) n0 = len;
+    mine += seq_cost(len, kt, ips);
+  }
+  long long before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  const long long total = __shfl_sync(0xffffffffu, before, 31);
+  before -= mine;
+  const int P = (int)min((long long)grid, total);  // runs that hold a tile
+  if (c >= P) return Walk(a, ips, kt, 0, 0, 0, 0);
+  const long long lo = div_tiles(total * c, P), hi = div_tiles(total * (c + 1), P);
+  int wb = b0, wlen = n0;
+  long long woff = lo - before;
+  const bool here = lo >= before && lo < before + mine;
+  if (here && per > 1) {
+    for (long long at = before; wb < b1; ++wb) {
+      wlen = seq_len(a, wb);
+      const long long w = seq_cost(wlen, kt, ips);
+      woff = lo - at;
+      if (woff < w) break;
+      at += w;
+    }
+  }
+  const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  wb = __shfl_sync(0xffffffffu, wb, src);
+  wlen = __shfl_sync(0xffffffffu, wlen, src);
+  woff = __shfl_sync(0xffffffffu, woff, src);
+  return Walk(a, ips, kt, wb, wlen, woff, hi - lo);
+}
+
+// The segment of a cluster CTA: its share of item blockIdx.x / cs.
+__device__ __forceinline__ Single find_share(const DecodeArgs& a, int cs, int ips, int kt, bool report) {
+  const int id = blockIdx.x / cs, rank = blockIdx.x % cs, b = id / ips, item = id % ips;
+  const int n = a.ctx_len[b];
+  const bool ok = n >= 0 && n <= a.s.L_ctx;
+  if (!ok && report && rank == 0 && item == 0 && (threadIdx.x & 31) == 0) flag_error(a.err, ERR_BAD_INDEX);
+  const int len = ok ? n : 0, nt = (len + kt - 1) / kt;
+  return Single{Segment{b, item, nt * rank / cs, nt * (rank + 1) / cs, nt, len}, false};
+}
+
+// CL: clusters of cs CTAs take one item each; else equal runs.
+template <typename T, int D, int RB, bool CL>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-              const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodeWs ws) {
+              const __grid_constant__ DecodeArgs a, const __grid_constant__ DecodeWs ws, int cs,
+              bool own_mass) {
   using C = Cfg<T, D, RB>;
   extern __shared__ char smem_raw[];
   char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -552,51 +704,15 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
   pdl_wait();
   pdl_trigger();                         // after the wait: the join kernel reads the lengths before its own
 
-  // This CTA's run: tiles [lo, hi) of the total of all sequences.  Every warp
-  // finds it for itself: a lane counts `per` sequences; the one whose count
-  // passes lo has the place.
-  const int per = (s.batch + 31) / 32, b0 = min(s.batch, lane * per), b1 = min(s.batch, b0 + per);
-  long long mine = 0;
-  int n0 = 0;                            // length of sequence b0
-#pragma unroll 4
-  for (int b = b0; b < b1; ++b) {
-    const int n = a.ctx_len[b];
-    const bool ok = n >= 0 && n <= s.L_ctx;
-    if (!ok && blockIdx.x == 0 && warp == 0) flag_error(a.err, ERR_BAD_INDEX);
-    const int len = ok ? n : 0;
-    if (b == b0) n0 = len;
-    mine += seq_cost(len, C::KT, ips);
-  }
-  long long before = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += v;
-  }
-  const long long total = __shfl_sync(0xffffffffu, before, 31);
-  before -= mine;
-  const int P = (int)min((long long)gridDim.x, total);  // runs that hold a tile
+  auto walk = [&] {
+    if constexpr (CL) return find_share(a, cs, ips, C::KT, warp == 0);
+    else return find_run(a, blockIdx.x, gridDim.x, ips, C::KT, blockIdx.x == 0 && warp == 0);
+  }();
   const int c = blockIdx.x;
-  if (c >= P) return;
-  const long long lo = div_tiles(total * c, P), hi = div_tiles(total * (c + 1), P);
-  int wb = b0, wlen = n0;
-  long long woff = lo - before;
-  const bool here = lo >= before && lo < before + mine;
-  if (here && per > 1) {
-    for (long long at = before; wb < b1; ++wb) {
-      wlen = seq_len(a, wb);
-      const long long w = seq_cost(wlen, C::KT, ips);
-      woff = lo - at;
-      if (woff < w) break;
-      at += w;
-    }
+  if constexpr (!CL) {
+    if (walk.left <= 0) return;          // the whole CTA: fewer tiles than CTAs
   }
-  const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-  wb = __shfl_sync(0xffffffffu, wb, src);
-  wlen = __shfl_sync(0xffffffffu, wlen, src);
-  woff = __shfl_sync(0xffffffffu, woff, src);
   __syncthreads();                       // the barriers are set up
-  Walk walk(a, ips, C::KT, wb, wlen, woff, hi - lo);
   Segment seg;
 
   if (warp == kWarps) {
@@ -644,7 +760,8 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
       for (int i = max(0, k - C::ST); i < k; ++i)
         for (uint32_t n = 0; n < 4096 && !mbar_try_wait(full + i % C::ST, (i / C::ST) & 1); ++n) {}
     }
-    return;
+    __syncwarp();
+    if constexpr (!CL) return;
   }
 
   // ---- computing warps
@@ -655,7 +772,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
   const float c2 = (float)(s.scale * 1.4426950408889634);
   int k = 0;
   bool dead = false;
-  while (walk.next(&seg)) {
+  while ((!CL || warp < kWarps) && walk.next(&seg)) {
     const int g = seg.item / nrb, r0 = (seg.item % nrb) * RB, n_rows = min(RB, s.G - r0);
     const size_t row0 = (size_t)seg.b * s.H + g * s.G + r0;  // the block's first (b, h)
     const T* q = reinterpret_cast<const T*>(a.Q) + row0 * D;
@@ -719,6 +836,14 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
       }
       if (w0 + C::COPIES < kWarps) named_bar_sync(1, kWarps * 32);
     }
+    if constexpr (CL) {                  // this CTA's state, for the cluster
+      if (warp == 0) {
+        if (lane < RB) s_ml[lane] = make_float2(M, L);
+        __syncwarp();
+        st8.each(lane, [&](int r, int col, float2 v) { store2(s_o + r * D + col, v); });
+      }
+      continue;
+    }
     if (warp != 0) continue;
     if (lane == 0) {                     // for the join kernel
       int* runs = ws.runs + ((size_t)seg.b * ips + seg.item) * 2;
@@ -749,6 +874,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
       });
     }
   }
+  if constexpr (CL) cluster_finish<T, D, RB>(a, ws, sm, walk.seg, cs, own_mass);
 }
 
 // The partials of one item: runs c0..c0 + n - 1 and their slots.
@@ -957,24 +1083,49 @@ cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
                           : tc_map_f32_2d(&mk, a.Kp, D, rows, C::KT) &&
                                 tc_map_f32_2d(&mv, a.Vp, D, rows, C::KT);
   if (!ok) return cudaErrorInvalidValue;
-  auto kern = decode_kernel<T, D, RB>;
-  cudaError_t e = allow_smem<decode_kernel<T, D, RB>>(C::SMEM);
-  if (e != cudaSuccess) return e;
-  const long long most = (long long)s.batch * items_per_seq(s) * ((s.L_ctx + C::KT - 1) / C::KT);
-  int P = tc_sm_count() * kCtasPerSm;
-  P = P < kMaxCtas ? P : kMaxCtas;
-  P = (int)(most < P ? (most > 0 ? most : 1) : P);
-  DL_LAUNCH(kern, P, kThreads, C::SMEM, st, mk, mv, a, w);
+  const int tiles = (s.L_ctx + C::KT - 1) / C::KT, fit = kCtasPerSm * tc_sm_count();
+  const long long items = (long long)s.batch * items_per_seq(s);
+  // Small enough for clusters?
+  int cs = 1;
+  while (cs < kMaxCluster && cs < tiles && items * cs * 2 <= fit) cs *= 2;
+  const bool clusters = items * cs <= fit &&
+                        tiles <= cs * (4 * items * cs >= 3 * fit ? kClusterTilesFull : kClusterTiles);
+  const bool own_mass = !a.tok_mass || (a.n_mass == s.H_kv && s.G <= RB);
+  if (clusters) {
+    cudaError_t e = allow_smem<decode_kernel<T, D, RB, true>>(C::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * cs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0] = cluster_of(cs);
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, decode_kernel<T, D, RB, true>, mk, mv, a, w, cs, own_mass);
+    if (e != cudaSuccess || own_mass) return e;
+  } else {
+    cudaError_t e = allow_smem<decode_kernel<T, D, RB, false>>(C::SMEM);
+    if (e != cudaSuccess) return e;
+    const long long most = items * tiles;
+    int P = fit < kMaxCtas ? fit : kMaxCtas;
+    P = (int)(most < P ? (most > 0 ? most : 1) : P);
+    auto kern = decode_kernel<T, D, RB, false>;
+    DL_LAUNCH(kern, P, kThreads, C::SMEM, st, mk, mv, a, w, 0, false);
+  }
   // masses: 1024 tokens a CTA, fewer while that leaves SMs idle (with two
   // batches of loads a thread the join's first 3 us are shared; a batch's
   // longest sequence must not take its time alone either)
   int chunks = 0;
   if (a.tok_mass && s.L_ctx > 0) {
     const int rows = s.H / a.n_mass, tj = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8;
-    const int dec = s.batch * a.n_mass, fit = (4 * tc_sm_count() + dec - 1) / dec;
+    const int dec = s.batch * a.n_mass, idle = (4 * tc_sm_count() + dec - 1) / dec;
     const int most = (s.L_ctx + kJoinThreads * tj - 1) / (kJoinThreads * tj);
     const int few = (s.L_ctx + 1023) / 1024;
-    chunks = fit > few ? fit : few;
+    chunks = idle > few ? idle : few;
     chunks = chunks < most ? chunks : most;
     chunks = chunks < 4096 ? chunks : 4096;
   }
@@ -995,7 +1146,8 @@ cudaError_t launch_decode_attn(const DecodeArgs& a, cudaStream_t st) {
       return s.G > 8 ? run_decode<__nv_bfloat16, 128, 16>(a, st) : run_decode<__nv_bfloat16, 128, 8>(a, st);
     return s.G > 8 ? run_decode<__nv_bfloat16, 64, 16>(a, st) : run_decode<__nv_bfloat16, 64, 8>(a, st);
   }
-  return s.d == 128 ? run_decode<float, 128, 8>(a, st) : run_decode<float, 64, 8>(a, st);
+  if (s.d == 128) return s.G > 2 ? run_decode<float, 128, 8>(a, st) : run_decode<float, 128, 2>(a, st);
+  return s.G > 2 ? run_decode<float, 64, 8>(a, st) : run_decode<float, 64, 2>(a, st);
 }
 
 }  // namespace dl

@@ -28,6 +28,7 @@
 // Moves: bound by HBM (each moved row is read and written once).  A warp
 // resolves 32 moves at a time, one per lane, then all lanes copy their rows in
 // 16-byte pieces, eight loads ahead of the stores.
+#include "cluster.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -51,23 +52,6 @@ __device__ __forceinline__ unsigned mass_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ unsigned cluster_rank() {
-  unsigned r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Value at the same shared-memory place of CTA `rank` of the cluster.
-__device__ __forceinline__ int peer_int(const int* p, unsigned rank) {
-  const unsigned here = static_cast<unsigned>(__cvta_generic_to_shared(p));
-  unsigned there;
-  int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
-  return v;
-}
 __device__ __forceinline__ int warp_inclusive(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -93,7 +77,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
   __shared__ int s_max[kEvWarps];
   const Shape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = cs > 1 ? (int)cluster_rank() : 0;
+  const int rank = cs > 1 ? cluster_rank() : 0;
   const int row = blockIdx.x / cs, b = row / a.n_mass;
   pdl_trigger();
   pdl_wait();
@@ -484,9 +468,7 @@ cudaError_t run_evict(const EvictArgs& a, int cs, int tiles, cudaStream_t st) {
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[0] = cluster_of(cs);
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;

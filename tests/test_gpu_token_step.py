@@ -262,6 +262,13 @@ DECODE_CASES = [
     ("bf16", 128, 1, 1, 4000, [4000], 1, 1.0),           # one long row over the whole grid
     ("fp32", 64, 1, 1, 3001, [3001], 1, 1.0),
     ("bf16", 64, 2, 2, 1, [1, 0], 2, 1.0),               # capacity of one token
+    ("bf16", 128, 2, 2, 9000, [9000, 0, 70], 2, 0.5),    # too long for clusters
+    ("bf16", 64, 3, 4, 8100, [5000, 8100], 1, 1.0),
+    ("bf16", 128, 12, 1, 6000, [6000, 5999], 1, 0.3),
+    ("fp32", 128, 2, 2, 5000, [4990, 33], 2, 0.0),
+    ("fp32", 64, 9, 1, 2100, [2100, 64], 1, 1.0),
+    ("fp32", 128, 2, 3, 3000, [2999], 3, 1.0),
+    ("bf16", 64, 1, 5, 150, [150, 20, 0] * 12, 5, 1.0),  # clusters of one CTA
 ]
 
 
