@@ -82,7 +82,8 @@ typedef struct {
  *   DL_FLAG_TOKEN_SIMT   dl_token_select on its CUDA-core kernel
  *   DL_FLAG_GATHER_SIMT  dl_sparse_attn_gather on its CUDA-core kernel
  *   DL_FLAG_PDL          every kernel launched with programmatic dependent
- *                        launch (measured no faster inside a CUDA graph)
+ *                        launch (measured no faster inside a CUDA graph; the
+ *                        token-by-token calls c1-c4 always are)
  *   DL_FLAG_SCORE_FP64   dl_block_select always on the fp64 scoring kernel
  *                        (skips the certified integer tensor-core scoring)
  * Process-wide; read by each later call at launch time.  No environment

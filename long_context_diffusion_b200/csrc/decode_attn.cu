@@ -988,6 +988,7 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
   const Shape& s = a.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int NW = kJoinThreads / 32;
+  pdl_trigger();
   if (blockIdx.x < s.batch * s.H) {
     __shared__ float s_m[NW], s_l[NW], s_w[kMaxCtas];
     __shared__ float4 s_o[kJoinThreads];
@@ -1104,7 +1105,7 @@ cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, decode_kernel<T, D, RB, true>, mk, mv, a, w, cs, own_mass);
     if (e != cudaSuccess || own_mass) return e;
   } else {
@@ -1114,7 +1115,7 @@ cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
     int P = fit < kMaxCtas ? fit : kMaxCtas;
     P = (int)(most < P ? (most > 0 ? most : 1) : P);
     auto kern = decode_kernel<T, D, RB, false>;
-    DL_LAUNCH(kern, P, kThreads, C::SMEM, st, mk, mv, a, w, 0, false);
+    DL_LAUNCH_DEPENDENT(kern, P, kThreads, C::SMEM, st, mk, mv, a, w, 0, false);
   }
   // masses: 1024 tokens a CTA, fewer while that leaves SMs idle (with two
   // batches of loads a thread the join's first 3 us are shared; a batch's

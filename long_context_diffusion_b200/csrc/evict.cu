@@ -472,7 +472,7 @@ cudaError_t run_evict(const EvictArgs& a, int cs, int tiles, cudaStream_t st) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, evict_select_kernel<CPL, VEC>, a, cs, tiles);
 }
 
@@ -513,8 +513,8 @@ cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {
   const int grid = (int)(want < most ? want : most);
 #define DL_COMPACT(CH_)                                                                           \
   do {                                                                                            \
-    if (wide) DL_LAUNCH((cache_compact_kernel<CH_, 32>), grid, 256, 0, st, a, groups, tasks);     \
-    else DL_LAUNCH((cache_compact_kernel<CH_, 8>), grid, 256, 0, st, a, groups, tasks);           \
+    if (wide) DL_LAUNCH_DEPENDENT((cache_compact_kernel<CH_, 32>), grid, 256, 0, st, a, groups, tasks);     \
+    else DL_LAUNCH_DEPENDENT((cache_compact_kernel<CH_, 8>), grid, 256, 0, st, a, groups, tasks);           \
   } while (0)
   const int pieces = s.d * (s.dtype == DL_BF16 ? 2 : 4) / 16;
   if (pieces == 8) DL_COMPACT(8);

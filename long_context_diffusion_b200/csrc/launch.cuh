@@ -16,6 +16,12 @@
 // graph's launch gaps are already small), so it is opt-in: the DL_FLAG_PDL
 // kernel flag (dl_set_kernel_flags) turns it on; otherwise kernels launch
 // plainly and pdl_wait() returns at once.
+// The token-by-token calls (dl_qk_norm_rope, dl_decode_attn, dl_evict_select,
+// dl_cache_compact) always use it: they run for 4 to 20 us, of which it hides
+// 1.5 to 2 (back to back, eager: norm + rotation of a block 6.2 -> 4.8 us, tiny
+// attention 8.2 -> 6.4, eviction plan 8.9 -> 6.8, 64 moves 6.2 -> 3.9).  In each
+// of their kernels some CTA always reaches pdl_wait(), so that its completion
+// implies its predecessors'.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -36,8 +42,7 @@ __device__ __forceinline__ void pdl_trigger() {
 
 inline bool pdl_enabled() { return (kernel_flags() & DL_FLAG_PDL) != 0; }
 
-// `dependent`: programmatic even without the flag, for the second kernel of one
-// call, whose launch and prologue then overlap the first.
+// `dependent`: programmatic even without the flag.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_as(bool dependent, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                       cudaStream_t st, Args&&... args) {

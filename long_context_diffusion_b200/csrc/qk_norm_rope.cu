@@ -465,9 +465,9 @@ cudaError_t run_rope(const RopeArgs& a, cudaStream_t st) {
   // eight columns that are rotated or left alone as a whole.
   if (tt == 8 && all >= 2ll * tc_sm_count() && a.rot_dim % 16 == 0) {
     if (a.interleaved)
-      DL_LAUNCH((qk_norm_rope_wide_kernel<T, D, true>), (unsigned)all, kWideThreads, 0, st, a, tiles);
+      DL_LAUNCH_DEPENDENT((qk_norm_rope_wide_kernel<T, D, true>), (unsigned)all, kWideThreads, 0, st, a, tiles);
     else
-      DL_LAUNCH((qk_norm_rope_wide_kernel<T, D, false>), (unsigned)all, kWideThreads, 0, st, a, tiles);
+      DL_LAUNCH_DEPENDENT((qk_norm_rope_wide_kernel<T, D, false>), (unsigned)all, kWideThreads, 0, st, a, tiles);
     return cudaGetLastError();
   }
   const int most = (n_rows * tt + RPP - 1) / RPP;
@@ -476,11 +476,11 @@ cudaError_t run_rope(const RopeArgs& a, cudaStream_t st) {
   const int per = (n_rows + (int)split - 1) / (int)split;
   const dim3 grid((unsigned)all, (n_rows + per - 1) / per);
   if (tt == 1) {
-    DL_LAUNCH((qk_norm_rope_kernel<T, D, 1, 1>), grid, kRopeThreads, 0, st, a, tiles, per);
+    DL_LAUNCH_DEPENDENT((qk_norm_rope_kernel<T, D, 1, 1>), grid, kRopeThreads, 0, st, a, tiles, per);
   } else if (per * tt <= RPP) {
-    DL_LAUNCH((qk_norm_rope_kernel<T, D, 8, 1>), grid, kRopeThreads, 0, st, a, tiles, per);
+    DL_LAUNCH_DEPENDENT((qk_norm_rope_kernel<T, D, 8, 1>), grid, kRopeThreads, 0, st, a, tiles, per);
   } else {
-    DL_LAUNCH((qk_norm_rope_kernel<T, D, 8, 4>), grid, kRopeThreads, 0, st, a, tiles, per);
+    DL_LAUNCH_DEPENDENT((qk_norm_rope_kernel<T, D, 8, 4>), grid, kRopeThreads, 0, st, a, tiles, per);
   }
   return cudaGetLastError();
 }

@@ -698,6 +698,168 @@ def test_two_streams_at_once(cuda_device):
         _check_decode(Q, K, V, table, lens, *out, torch.zeros(3, 4, 700), mass, 0.0, "bf16", 4, 4)
 
 
+def _busy_run(dev, sync, body_streams=None):
+    """Steps that leave no gap between the calls and the framework's and
+    torch's own work on the same buffers; `sync` waits after every one."""
+    B, H, H_kv, d, L, layers = 3, 6, 2, 64, 140, 2
+    desc, step, table, pools, w = _token_model(dev, budget=64, decay=0.5)
+    width = (H + 2 * H_kv) * d
+    x = [_normal(66000 + l, B, 40, width, dtype=torch.bfloat16).to(dev) for l in range(layers)]
+    base = torch.arange(40, dtype=torch.int32, device=dev).expand(B, 40).contiguous()
+    q = torch.empty(B, H, 40, d, dtype=torch.bfloat16, device=dev)
+    wait = torch.cuda.synchronize if sync else (lambda: None)
+    n_blk = desc.n_pages
+    kbar = torch.zeros(B, H_kv, n_blk, d, device=dev)
+    seen = []
+    for l in range(layers):
+        step.append(l, x[l], base, *w[l], *pools[l], table, q)
+        wait()
+    step.advance()
+    tok = torch.empty(B, 1, width, dtype=torch.bfloat16, device=dev)
+    pos = torch.full((B, 1), 39, dtype=torch.int32, device=dev)
+    for i in range(30):
+        pos.add_(1)
+        for l in range(layers):
+            torch.add(x[l][:, i:i + 1], 0.25 * l, out=tok)
+            wait()
+            O = step.attend(l, tok, pos, *w[l], *pools[l], table)
+            wait()
+            seen += [O.clone(), step.lse[l].clone()]
+            O.zero_()
+            tok.zero_()
+            # a kernel of the framework between two of the calls
+            new = x[l][:, :2, :H_kv * d].reshape(B, 2, H_kv, d).transpose(1, 2).contiguous()
+            dl.dl_cache_write(desc, new, new, torch.full((B,), i % 20, dtype=torch.int32, device=dev), table, *pools[l], kbar)
+            wait()
+        if i % 3 == 2:
+            step.evict([p[0] for p in pools], [p[1] for p in pools], table)
+        else:
+            step.advance()
+        wait()
+        seen += [step.start.clone(), *(t.clone() for t in step.tok_mass), *(t.clone() for t in step.tok_pos)]
+    assert dl.dl_get_status() == dl.DL_OK
+    return seen + [t for p in pools for t in p]
+
+
+def test_calls_without_gaps_see_each_others_results(cuda_device):
+    """The calls are launched programmatically (their start overlaps the end of
+    what comes before): with nothing waiting between them, torch's kernels and
+    the framework's on the same buffers, they give what they give when every
+    call is waited for."""
+    for a, b in zip(_busy_run(cuda_device, False), _busy_run(cuda_device, True)):
+        assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
+
+
+def test_captured_on_forked_streams(cuda_device):
+    """A capture that forks: two sequences' decodings on two streams between an
+    append and an eviction on the first; replayed twice on new inputs."""
+    dev, H_kv, d, L = cuda_device, 2, 64, 200
+    desc = _desc(1, 4, H_kv, d, L, "bf16", n_slots=4)
+    table = torch.arange(4, dtype=torch.int32, device=dev)[None]
+    K, V = (_normal(67000 + j, 4, H_kv, 64, d, dtype=torch.bfloat16).to(dev) for j in range(2))
+    x = torch.zeros(1, 1, 8 * d, dtype=torch.bfloat16, device=dev)
+    pos, start, end, new = (torch.zeros(1, dtype=torch.int32, device=dev) for _ in range(4))
+    Q = torch.empty(1, 4, 1, d, dtype=torch.bfloat16, device=dev)
+    mass = torch.zeros(1, H_kv, L, device=dev)
+    out = [torch.empty(1, 4, d, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    ws = [pipeline.workspace(desc, dev) for _ in range(2)]
+    plan = pipeline.eviction_buffers(desc, H_kv, 120, dev)
+    side = torch.cuda.Stream()
+
+    def body():
+        dl.dl_qk_norm_rope(desc, x, pos[None], None, None, 1e-6, None, Q, start=start, page_table=table, K_pool=K,
+                           V_pool=V, end=end, tok_mass=mass)
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        dl.dl_decode_attn(desc, Q, K, V, table, end, out[0], None, ws[0], tok_mass=mass, decay=0.5)
+        dl.dl_decode_attn(desc, Q, K, V, table, start, out[1], None, ws[1], stream=side)
+        main.wait_stream(side)
+        pipeline.evict(desc, K, V, table, end, new, mass, budget=120, n_first=1, n_recent=4, plan=plan)
+
+    state = [K.clone(), V.clone(), mass.clone()]
+
+    def reset(i):
+        for t, s in zip((K, V, mass), state):
+            t.copy_(s)
+        x.copy_(_normal(67010 + i, 1, 1, 8 * d, dtype=torch.bfloat16))
+        pos.fill_(150 + i), start.fill_(150 + i)
+
+    want = []
+    for i in range(2):
+        reset(i)
+        body()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (*out, K, V, mass, new, end, *plan)])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body()
+    for i in range(2):
+        reset(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((*out, K, V, mass, new, end, *plan), want[i]):
+            assert torch.equal(a, b)
+    assert dl.dl_get_status() == dl.DL_OK
+
+
+@pytest.mark.parametrize("what", ["dtype", "size", "strided", "host", "rows"])
+def test_buffers_that_do_not_fit_are_refused(what, cuda_device):
+    """Wrong tensors never reach the library: ValueError, nothing written."""
+    dev, B, H, H_kv, d, L = cuda_device, 2, 4, 2, 64, 100
+    desc = _desc(B, H, H_kv, d, L, "bf16")
+    good = dict(Q=torch.zeros(B, H, d, dtype=torch.bfloat16, device=dev),
+                K_pool=torch.zeros(desc.n_slots, H_kv, 64, d, dtype=torch.bfloat16, device=dev),
+                V_pool=torch.zeros(desc.n_slots, H_kv, 64, d, dtype=torch.bfloat16, device=dev),
+                page_table=torch.zeros(B, 2, dtype=torch.int32, device=dev),
+                ctx_len=torch.zeros(B, dtype=torch.int32, device=dev),
+                O=torch.full((B, H, d), 7.0, dtype=torch.bfloat16, device=dev), lse=torch.zeros(B, H, device=dev),
+                ws=pipeline.workspace(desc, dev), tok_mass=torch.zeros(B, H_kv, L, device=dev))
+    for name in good:
+        bad = dict(good)
+        t = bad[name]
+        if what == "dtype":
+            if name == "ws":
+                continue
+            bad[name] = t.double()
+        elif what == "size":
+            if name == "ws":
+                continue
+            bad[name] = torch.zeros(t.numel() + 1, dtype=t.dtype, device=dev)[1:-1].clone() if name != "tok_mass" \
+                else torch.zeros(B, H_kv, L + 1, device=dev)
+        elif what == "strided":
+            wide = torch.zeros(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype, device=dev)
+            bad[name] = wide[..., ::2]
+        elif what == "host":
+            bad[name] = t.cpu()
+        elif name != "tok_mass":
+            continue
+        else:
+            bad[name] = torch.zeros(B, L, H_kv, device=dev)   # rows and tokens swapped
+        with pytest.raises((ValueError, dl.DLError)):
+            dl.dl_decode_attn(desc, **bad)
+    torch.cuda.synchronize()
+    assert (good["O"] == 7).all()
+    dl.dl_decode_attn(desc, **good)
+    assert dl.dl_get_status() == dl.DL_OK and (good["O"] == 0).all()
+
+
+def test_streams_by_object_and_by_handle(cuda_device):
+    desc = _desc(1, 2, 2, 64, 64, "fp32")
+    x = _normal(68000, 1, 3, 6 * 64).to(cuda_device)
+    pos = torch.arange(3, dtype=torch.int32, device=cuda_device)[None]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for stream in (None, st, st.cuda_stream):
+        o = [torch.empty(1, 2, 3, 64, device=cuda_device) for _ in range(3)]
+        torch.cuda.synchronize()
+        dl.dl_qk_norm_rope(desc, x, pos, None, None, 0.0, None, *o, stream=stream)
+        torch.cuda.synchronize()
+        outs.append(o)
+    for o in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+
+
 def test_sink_masses_cut_a_denoising_context(cuda_device):
     """The diffusion path: column masses of a denoising step (dl_sink_mass)
     decide which context stays; the cut cache serves dl_pool_keys and the

@@ -136,3 +136,20 @@ def test_host_tensors_are_refused():
         dl.dl_evict_select(desc, m, None, i, 100, 0, 0, None, None, i, i)
     with pytest.raises(ValueError):
         dl.dl_cache_compact(desc, m, m, i, i, q, q)
+
+
+def test_wrong_objects_are_refused():
+    desc = _desc(batch=1, H=1, H_kv=1, d=64)
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        dl.dl_qk_norm_rope(desc, 3, None, None, None, 1e-6, None, None)
+    with pytest.raises(TypeError):
+        dl.dl_decode_attn("desc", None, None, None, None, None, None, None, None)
+    with pytest.raises(ValueError):
+        dl.dl_evict_select(desc, torch.zeros(1, 1, 1000), None, None, 1 << 40, 0, 0, None, None, None, None)
+    with pytest.raises(ValueError, match="current CUDA device"):  # nothing but None: no device
+        dl.dl_cache_compact(desc, None, None, None, None, None, None)
+
+
+def test_the_extension_checks_its_argument_count():
+    with pytest.raises(TypeError, match="number of arguments"):
+        _abi._calls.decode_attn(_desc())
