@@ -382,7 +382,7 @@ dl_status dl_block_scores_noalloc(const dl_attn_desc* desc, const void* Q_dec,
  *   - These calls do not keep the pooled keys of dl_pool_keys up to date:
  *     call dl_pool_keys before the next block selection over this cache.
  *   - Buffers that a call writes must not overlap any other buffer of the
- *     call. */
+ *     call, and pages that it writes must belong to one sequence only. */
 
 /* (c1) Per-head norm of queries and keys, position rotation, head split and
  * cache append, in one pass over the projection's output.
@@ -427,7 +427,7 @@ dl_status dl_qk_norm_rope(const dl_attn_desc* desc, const void* qkv, int64_t qkv
  *   o_h = sum_t e^{a_t - lse} v_t
  * fp32 accumulation, O rounded to nearest-even in the input dtype.  The new
  * token attends to itself when its own key is in the cache (c1 puts it there).
- * n = 0: O = 0 and lse = -infinity.  A length outside 0..L_ctx counts as 0,
+ * L_ctx <= 2^30.  n = 0: O = 0 and lse = -infinity.  A length outside 0..L_ctx counts as 0,
  * and a page slot out of range makes that sequence's results unspecified;
  * both report DL_ERR_BAD_INDEX.
  *   Q        [batch][H][d], O [batch][H][d], 16-byte aligned (desc->L_q == 1)
@@ -479,7 +479,7 @@ dl_status dl_evict_select(const dl_attn_desc* desc, const float* tok_mass, const
  * holes are distinct and are no fills (otherwise which move wins is
  * unspecified).  A move whose index is outside 0..L_ctx-1 or whose page slot
  * is out of range is skipped, a count outside 0..max_move is clamped; both
- * report DL_ERR_BAD_INDEX.  Pages must not be shared between sequences. */
+ * report DL_ERR_BAD_INDEX. */
 dl_status dl_cache_compact(const dl_attn_desc* desc, const int32_t* hole_idx,
                            const int32_t* fill_idx, const int32_t* move_cnt, int max_move,
                            int n_mass, const int32_t* page_table, void* K_pool, void* V_pool,

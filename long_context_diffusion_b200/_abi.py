@@ -287,7 +287,8 @@ def _bind_calls(of):
 
 
 _calls = _load_calls()
-_bind_calls(lib)
+if hasattr(torch.Tensor, "__dlpack_c_exchange_api__"):  # else these four calls say what is missing
+    _bind_calls(lib)
 
 
 def _raw(stream):

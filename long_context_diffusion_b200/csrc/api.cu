@@ -165,7 +165,7 @@ dl_status dl_workspace_size(const dl_attn_desc* desc, size_t* bytes) {
   need = x > need ? x : need;
   x = dl::sinks_workspace(s);
   need = x > need ? x : need;
-  if (s.L_q == 1) {  // the only descriptors dl_decode_attn takes
+  if (s.L_q == 1 && s.L_ctx <= dl::kDecodeMaxCtx) {  // the descriptors dl_decode_attn takes
     x = dl::decode_workspace(s, true);
     need = x > need ? x : need;
   }
@@ -493,6 +493,8 @@ dl_status dl_decode_attn(const dl_attn_desc* desc, const void* Q, const void* K_
   dl_status st = check_desc(desc, &s);
   if (st != DL_OK) return st;
   if (s.L_q != 1) return fail(DL_ERR_UNSUPPORTED, "dl_decode_attn: L_q=%d (need 1)", s.L_q);
+  if (s.L_ctx > dl::kDecodeMaxCtx)
+    return fail(DL_ERR_UNSUPPORTED, "dl_decode_attn: L_ctx=%d (need <= 2^30)", s.L_ctx);
   if (!Q || !K_pool || !V_pool || (!page_table && s.n_pages > 0) || !ctx_len || !O)
     return fail(DL_ERR_INVALID_ARG, "dl_decode_attn: NULL pointer");
   if (!aligned16(Q) || !aligned16(K_pool) || !aligned16(V_pool) || !aligned16(O))

@@ -50,7 +50,7 @@ struct Call {
   Call(const char* name_, PyObject* const* args_, Py_ssize_t nargs, Py_ssize_t want)
       : name(name_), args(args_) {
     if (!g_rope) {
-      fail(PyExc_RuntimeError, "bind() has not been called");
+      fail(PyExc_RuntimeError, "not bound: this torch has no DLPack exchange table on torch.Tensor");
     } else if (nargs != want) {
       fail(PyExc_TypeError, "wrong number of arguments");
     } else {

@@ -162,6 +162,7 @@ struct DecodeArgs {
   void* ws;
   unsigned* err;
 };
+constexpr int kDecodeMaxCtx = 1 << 30;  // tokens: tile arithmetic stays in 32 bits
 size_t decode_workspace(const Shape& s, bool mass);
 cudaError_t launch_decode_attn(const DecodeArgs& a, cudaStream_t st);
 

@@ -295,6 +295,9 @@ class TokenStep:
     a page table, each sequence with its own length, optionally kept within a
     budget of cached tokens per sequence.
 
+    Sequences whose prompts differ in length are appended padded; their true
+    lengths are then written to `start` (the padding is overwritten).
+
     A step: for every layer `attend` (norm, rotation and cache append of the
     new token, then its attention); then once `advance`, or `evict`, which also
     cuts every cache to the budget.  A prompt enters with `append`, followed by
@@ -352,6 +355,8 @@ class TokenStep:
 
     def evict(self, k_pools: List, v_pools: List, page_table, stream=None):
         """Ends a step and cuts every layer's cache to the budget."""
+        if not self.budget:
+            raise ValueError("TokenStep was made without a budget: nothing to evict by")
         for l in range(self.n_layers):
             evict(self.desc, k_pools[l], v_pools[l], page_table, self.end, self.start,
                   self.tok_mass[l], budget=self.budget, n_first=self.n_first,

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import long_context_diffusion_b200 as dl
-from long_context_diffusion_b200 import _abi
+from long_context_diffusion_b200 import _abi, pipeline
 
 FAKE = 0x10000
 ODD = 0x10008
@@ -115,10 +115,31 @@ def test_descriptor_is_checked(name, args):
         assert _call(name, _desc(**kw), args)[0] in (dl.DL_ERR_INVALID_ARG, dl.DL_ERR_UNSUPPORTED), kw
 
 
-def test_workspace_grows_only_for_single_token_descriptors():
-    # the same as ever for a decode block, and enough for the logits for one token
+def test_decode_attn_capacity_limit():
+    big = _desc(L_ctx=(1 << 30) + 1, n_pages=(1 << 24) + 1)
+    st, msg = _call("dl_decode_attn", big, DECODE)
+    assert st == dl.DL_ERR_UNSUPPORTED and "L_ctx" in msg
+
+
+@pytest.mark.parametrize("name,args", [("dl_decode_attn", DECODE), ("dl_cache_compact", COMPACT)])
+def test_pools_of_2_31_rows_are_refused(name, args):
+    st, msg = _call(name, _desc(n_slots=1 << 23), args)
+    assert st == dl.DL_ERR_UNSUPPORTED and "rows" in msg
+
+
+def test_workspace_holds_the_dot_products_of_single_token_descriptors():
     one = dl.dl_workspace_size(_desc())
-    assert one >= 0 and one % 256 == 0
+    assert one % 256 == 0 and one >= 2 * 28 * 1024 * 4      # batch, H, L_ctx padded to tiles
+    # DECODE's call is refused with one byte less than it needs
+    with_mass = DECODE | dict(ws_bytes=2 * 28 * 1024 * 4)
+    assert _call("dl_decode_attn", _desc(), with_mass)[0] == dl.DL_ERR_WORKSPACE
+
+
+def test_token_step_without_a_budget_has_nothing_to_evict():
+    step = object.__new__(pipeline.TokenStep)
+    step.budget = 0
+    with pytest.raises(ValueError, match="budget"):
+        step.evict([], [], None)
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="a host without a GPU")
