@@ -34,8 +34,12 @@
 // high, 8-15 low), with 9-16 they take two.  The instruction is used because
 // a tile has at most 16 useful rows and the operands' conversion and traffic,
 // not the products, are what fills an SM here.
-// fp32: the same walk on the CUDA cores (exact products, fp32 sums): lane =
-// (key, quarter of d) for S, lane = four columns for O.
+// fp32: the same walk on the CUDA cores: lane = (key, quarter of d) for S, lane =
+// four columns for O.  The dot products are summed in fp64 and stay so until
+// the reference is subtracted: beside a sink's logit of 35 one fp32 rounding of
+// a logit is 1e-6 of its weight, as large as all other errors together.  (A
+// tile's 32 KB take 1400 cycles of an SM's share of HBM, its fp64 sums 512 with
+// eight heads.)
 //
 // Weights.  With c = scale log2 e and a maximum m of the dot products x, the
 // reference is M = m c rounded once, and p = 2^(x c - M) in one fused
@@ -73,6 +77,7 @@ constexpr int kMaxCluster = 8;
 // tiles 18.3 to 21.4, of 16 tiles 28.1 to 31.2).
 constexpr int kClusterTiles = 4, kClusterTilesFull = 16;
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr double kLog2e = 1.4426950408889634;
 
 // Query heads per item block: 8; 16 for bf16 groups of more than 8; 2 for fp32
 // groups of at most 2 (on the CUDA cores empty rows cost as much as others).
@@ -95,7 +100,7 @@ struct DecodeWs {
   float* po;         // [2 kMaxCtas][RB][d] unnormalised partial outputs
   float2* pml;       // [2 kMaxCtas][RB] (reference, sum)
   float2* norm;      // [batch][H] (reference, 1 / sum) of the items finished in one run
-  float* logit;      // [batch][H][Lp] dot products (with masses)
+  void* logit;       // [batch][H][Lp] dot products (with masses): fp32, fp64 of fp32 keys
   int Lp;
 };
 
@@ -110,10 +115,23 @@ size_t carve(const Shape& s, bool mass, void* ws, DecodeWs* w) {
   d.po = reinterpret_cast<float*>(take((size_t)2 * kMaxCtas * rb * s.d * 4));
   d.pml = reinterpret_cast<float2*>(take((size_t)2 * kMaxCtas * rb * 8));
   d.norm = reinterpret_cast<float2*>(take((size_t)s.batch * s.H * 8));
-  d.logit = reinterpret_cast<float*>(take(mass ? (size_t)s.batch * s.H * d.Lp * 4 : 0));
+  d.logit = take(mass ? (size_t)s.batch * s.H * d.Lp * (s.dtype == DL_BF16 ? 4 : 8) : 0);
   if (w) *w = d;
   return at;
 }
+
+// Dot products in the workspace, and the exponent of a weight from one.
+template <typename T> struct Logit;
+template <> struct Logit<__nv_bfloat16> {
+  using Type = float;
+  __device__ __forceinline__ static float exponent(float x, float c2, double, float M) { return fmaf(x, c2, -M); }
+};
+template <> struct Logit<float> {
+  using Type = double;
+  __device__ __forceinline__ static float exponent(double x, float, double c2d, float M) {
+    return (float)fma(x, c2d, -(double)M);
+  }
+};
 
 // Cached tokens of sequence b; a length out of range counts as 0.
 __device__ __forceinline__ int seq_len(const DecodeArgs& a, int b) {
@@ -217,8 +235,8 @@ struct Cfg {
   // states of the other warps at a segment's end: all three at once, or one by one
   static constexpr int COPIES = BF16 && RB == 8 ? 3 : 1;
   static constexpr int O_OFF = ST * STAGE;
-  static constexpr int Q_OFF = O_OFF + COPIES * RB * D * 4;        // fp32 rows of Q
-  static constexpr int P_OFF = Q_OFF + (BF16 ? 0 : RB * D * 4);    // fp32 weights [warp][RB][8]
+  static constexpr int Q_OFF = O_OFF + COPIES * RB * D * 4;        // fp32 keys: rows of Q in fp64
+  static constexpr int P_OFF = Q_OFF + (BF16 ? 0 : RB * D * 8);    // fp32 keys: weights [warp][RB][8]
   static constexpr int ML_OFF = P_OFF + (BF16 ? 0 : kWarps * RB * 8 * 4);
   static constexpr int BAR_OFF = ML_OFF + kWarps * RB * 8;
   static constexpr int MISC_OFF = BAR_OFF + 2 * ST * 8;            // info [ST], abort
@@ -417,7 +435,7 @@ struct StateF32 {
   static constexpr int KS = 32 / CH;        // keys taken at a time by the P V lanes
   float o[RB][4];
   float m[RB], l[RB];                       // l: of this lane's key
-  const float* sq;                          // Q rows in shared memory [RB][D]
+  const double* sq;                         // Q rows in shared memory [RB][D]
   float* sp;                                // this warp's weights [RB][8]
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -430,19 +448,21 @@ struct StateF32 {
     return (c >> 3) * (32 * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
   }
   __device__ __forceinline__ void tile(const char* ks, const char* vs, int warp, int lane, int valid,
-                                       float c2, float* logit, int Lp, int n_rows) {
+                                       float c2, double c2d, double* logit, int Lp, int n_rows) {
     const int kk = lane & 7, key = warp * 8 + kk, dq = lane >> 3;
-    float x[RB];
+    double x[RB];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) x[r] = 0.0f;
+    for (int r = 0; r < RB; ++r) x[r] = 0.0;
 #pragma unroll
     for (int j = 0; j < CH / 4; ++j) {
       const int c = 4 * j + dq;
       const float4 k = *reinterpret_cast<const float4*>(ks + chunk_at(key, c));
+      const double k0 = k.x, k1 = k.y, k2 = k.z, k3 = k.w;
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
-        const float4 q = *reinterpret_cast<const float4*>(sq + r * D + 4 * c);
-        x[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, x[r]))));
+        const double2 p = *reinterpret_cast<const double2*>(sq + r * D + 4 * c);
+        const double2 q = *reinterpret_cast<const double2*>(sq + r * D + 4 * c + 2);
+        x[r] = fma(p.x, k0, fma(p.y, k1, fma(q.x, k2, fma(q.y, k3, x[r]))));
       }
     }
     const bool ok = key < valid;
@@ -452,9 +472,9 @@ struct StateF32 {
     for (int r = 0; r < RB; ++r) {
       x[r] += __shfl_xor_sync(0xffffffffu, x[r], 8);
       x[r] += __shfl_xor_sync(0xffffffffu, x[r], 16);
-      x[r] = ok ? x[r] : -INFINITY;
+      if (!ok) x[r] = -INFINITY;
       if (logit && dq == 0 && r < n_rows) logit[(size_t)r * Lp + key] = x[r];
-      float t = x[r];
+      float t = (float)x[r];
 #pragma unroll
       for (int w = 1; w < 8; w <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, w));
       top[r] = fmaxf(m[r], t);
@@ -473,7 +493,8 @@ struct StateF32 {
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
-      const float p = ex2_approx(fmaf(x[r], c2, m[r] == -INFINITY ? 0.0f : -__fmul_rn(m[r], c2)));
+      const float M = m[r] == -INFINITY ? 0.0f : __fmul_rn(m[r], c2);
+      const float p = ex2_approx((float)fma(x[r], c2d, -(double)M));
       l[r] += p;
       if (dq == (r & 3)) sp[r * 8 + kk] = p;
     }
@@ -607,15 +628,17 @@ __device__ __forceinline__ void cluster_finish(const DecodeArgs& a, const Decode
   }
   if (cs > 1) cluster_sync(); else __syncthreads();  // no CTA leaves while its state is read
   if (!a.tok_mass || !own_mass) return;
-  const float c2 = (float)(s.scale * 1.4426950408889634);
+  const float c2 = (float)(s.scale * kLog2e);
   float* mass = a.tok_mass + ((size_t)seg.b * s.H_kv + g) * s.L_ctx;
-  const float* x = ws.logit + row0 * ws.Lp;
+  using X = typename Logit<T>::Type;
+  const X* x = static_cast<const X*>(ws.logit) + row0 * ws.Lp;
+  const double c2d = s.scale * kLog2e;
   for (int t = seg.t0 * C::KT + tid; t < min(seg.len, seg.t1 * C::KT); t += kThreads) {
     const float old = a.decay != 0.0f ? mass[t] : 0.0f;
     float sum = 0.0f;
 #pragma unroll 4
     for (int r = 0; r < n_rows; ++r)
-      sum = fmaf(ex2_approx(fmaf(x[(size_t)r * ws.Lp + t], c2, -s_norm[r].x)), s_norm[r].y, sum);
+      sum = fmaf(ex2_approx(Logit<T>::exponent(x[(size_t)r * ws.Lp + t], c2, c2d, s_norm[r].x)), s_norm[r].y, sum);
     mass[t] = a.decay == 0.0f ? sum : fmaf(a.decay, old, sum);
   }
 }
@@ -769,7 +792,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
   State st8;
   float* s_o = reinterpret_cast<float*>(sm + C::O_OFF);
   float2* s_ml = reinterpret_cast<float2*>(sm + C::ML_OFF);
-  const float c2 = (float)(s.scale * 1.4426950408889634);
+  const float c2 = (float)(s.scale * kLog2e);
   int k = 0;
   bool dead = false;
   while ((!CL || warp < kWarps) && walk.next(&seg)) {
@@ -779,9 +802,9 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     if constexpr (C::BF16) {
       st8.load_q(q, n_rows, lane);
     } else {
-      float* sq = reinterpret_cast<float*>(sm + C::Q_OFF);
+      double* sq = reinterpret_cast<double*>(sm + C::Q_OFF);
       named_bar_sync(1, kWarps * 32);  // the last segment's rows are no longer read
-      for (int e = tid; e < RB * D; e += kWarps * 32) sq[e] = e < n_rows * D ? q[e] : 0.0f;
+      for (int e = tid; e < RB * D; e += kWarps * 32) sq[e] = e < n_rows * D ? (double)q[e] : 0.0;
       named_bar_sync(1, kWarps * 32);
       st8.sq = sq;
       st8.sp = reinterpret_cast<float*>(sm + C::P_OFF) + warp * RB * 8;
@@ -792,13 +815,14 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
       if (!dead) dead = !mbar_wait(full + st, (k / C::ST) & 1, abort_flag);
       if (__any_sync(0xffffffffu, dead)) { dead = true; continue; }
       const int valid = info[st];
-      float* logit = a.tok_mass ? ws.logit + row0 * ws.Lp + (size_t)t * C::KT : nullptr;
+      using X = typename Logit<T>::Type;
+      X* logit = a.tok_mass ? static_cast<X*>(ws.logit) + row0 * ws.Lp + (size_t)t * C::KT : nullptr;
       if constexpr (C::BF16) {
         const uint32_t ks = smem_u32(sm + st * C::STAGE);
         st8.tile(ks, ks + C::HALF, warp, lane, valid, c2, logit, ws.Lp, n_rows);
       } else {
         const char* ks = sm + st * C::STAGE;
-        st8.tile(ks, ks + C::HALF, warp, lane, valid, c2, logit, ws.Lp, n_rows);
+        st8.tile(ks, ks + C::HALF, warp, lane, valid, c2, s.scale * kLog2e, logit, ws.Lp, n_rows);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + st);
@@ -911,9 +935,10 @@ __device__ __forceinline__ float2 row_norm(const DecodeArgs& a, const DecodeWs& 
 
 // CTA `id` of the masses: one of `chunks` of a decision row.  A thread has
 // eight logits in flight, of 8 / QR tokens and QR rows.
-template <int QR>
+template <typename T, int QR>
 __device__ __forceinline__ void add_masses(const DecodeArgs& a, const DecodeWs& ws, int rb, int id,
                                            int chunks) {
+  using X = typename Logit<T>::Type;
   constexpr int NW = kJoinThreads / 32, TJ = 8 / QR;
   __shared__ float2 s_norm[64];          // 64 rows at a time
   const Shape& s = a.s;
@@ -924,13 +949,14 @@ __device__ __forceinline__ void add_masses(const DecodeArgs& a, const DecodeWs& 
   const int n = seq_len(a, b);
   if (first >= n) return;
   float* mass = a.tok_mass + ((size_t)b * a.n_mass + m) * s.L_ctx;
-  const float c2 = (float)(s.scale * 1.4426950408889634);
+  const double c2d = s.scale * kLog2e;
+  const float c2 = (float)c2d;
   pdl_wait();
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += 64) {
     const int nr = min(64, rows - r0);
     const float decay = r0 == 0 ? a.decay : 1.0f;
-    const float* x = ws.logit + ((size_t)b * s.H + h0 + r0) * ws.Lp;
+    const X* x = static_cast<const X*>(ws.logit) + ((size_t)b * s.H + h0 + r0) * ws.Lp;
     bool sums = false;
 #pragma unroll 1
     for (int t0 = first; t0 < n; t0 += step) {
@@ -942,7 +968,7 @@ __device__ __forceinline__ void add_masses(const DecodeArgs& a, const DecodeWs& 
       }
 #pragma unroll 1
       for (int q0 = 0; q0 < nr; q0 += QR) {
-        float v[QR][TJ];
+        X v[QR][TJ];
 #pragma unroll
         for (int q = 0; q < QR; ++q)
 #pragma unroll
@@ -963,7 +989,7 @@ __device__ __forceinline__ void add_masses(const DecodeArgs& a, const DecodeWs& 
           if (q0 + q >= nr) continue;
           const float2 norm = s_norm[q0 + q];
 #pragma unroll
-          for (int j = 0; j < TJ; ++j) sum[j] = fmaf(ex2_approx(fmaf(v[q][j], c2, -norm.x)), norm.y, sum[j]);
+          for (int j = 0; j < TJ; ++j) sum[j] = fmaf(ex2_approx(Logit<T>::exponent(v[q][j], c2, c2d, norm.x)), norm.y, sum[j]);
         }
       }
 #pragma unroll
@@ -1066,10 +1092,10 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
   }
   // ---- masses
   const int id = blockIdx.x - s.batch * s.H, rows = s.H / a.n_mass;
-  if (rows > 4) add_masses<8>(a, ws, rb, id, chunks);
-  else if (rows > 2) add_masses<4>(a, ws, rb, id, chunks);
-  else if (rows > 1) add_masses<2>(a, ws, rb, id, chunks);
-  else add_masses<1>(a, ws, rb, id, chunks);
+  if (rows > 4) add_masses<T, 8>(a, ws, rb, id, chunks);
+  else if (rows > 2) add_masses<T, 4>(a, ws, rb, id, chunks);
+  else if (rows > 1) add_masses<T, 2>(a, ws, rb, id, chunks);
+  else add_masses<T, 1>(a, ws, rb, id, chunks);
 }
 
 template <typename T, int D, int RB>
