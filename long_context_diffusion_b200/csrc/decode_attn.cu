@@ -1001,8 +1001,9 @@ __device__ __forceinline__ void add_masses(const DecodeArgs& a, const DecodeWs& 
   }
 }
 
-// CTAs [0, batch * H): join the partials of one query row (or write an empty
-// sequence's row).  The others: masses, `chunks` CTAs a decision row.
+// The last batch * H CTAs: join the partials of one query row (or write an
+// empty sequence's row).  Those before them, which take longer: masses, `chunks`
+// CTAs a decision row.
 // Bound by latency: chains of dependent loads, and the first fetch of the
 // code, so loops are short rather than unrolled.  What depends on the lengths
 // alone is done before the wait for the main kernel; each chain's bulk loads
@@ -1015,11 +1016,12 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int NW = kJoinThreads / 32;
   pdl_trigger();
-  if (blockIdx.x < s.batch * s.H) {
+  const int mass_ctas = s.batch * a.n_mass * chunks;
+  if ((int)blockIdx.x >= mass_ctas) {
     __shared__ float s_m[NW], s_l[NW], s_w[kMaxCtas];
     __shared__ float4 s_o[kJoinThreads];
     constexpr int CH = D / 4, GR = kJoinThreads / CH, U = 5;
-    const int row = blockIdx.x, b = row / s.H, h = row % s.H;
+    const int row = blockIdx.x - mass_ctas, b = row / s.H, h = row % s.H;
     const int n = seq_len(a, b);
     const int col = tid % CH, grp = tid / CH;  // thread = (run group, four columns)
     pdl_wait();
@@ -1091,7 +1093,7 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
     return;
   }
   // ---- masses
-  const int id = blockIdx.x - s.batch * s.H, rows = s.H / a.n_mass;
+  const int id = blockIdx.x, rows = s.H / a.n_mass;
   if (rows > 4) add_masses<T, 8>(a, ws, rb, id, chunks);
   else if (rows > 2) add_masses<T, 4>(a, ws, rb, id, chunks);
   else if (rows > 1) add_masses<T, 2>(a, ws, rb, id, chunks);
@@ -1157,8 +1159,7 @@ cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
     chunks = chunks < 4096 ? chunks : 4096;
   }
   auto join = decode_join_kernel<T, D>;
-  DL_LAUNCH_DEPENDENT(join, s.batch * s.H + s.batch * a.n_mass * chunks, kJoinThreads, 0, st, a, w, RB,
-                      chunks > 0 ? chunks : 1);
+  DL_LAUNCH_DEPENDENT(join, s.batch * s.H + s.batch * a.n_mass * chunks, kJoinThreads, 0, st, a, w, RB, chunks);
   return cudaGetLastError();
 }
 
