@@ -1145,15 +1145,15 @@ cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
     auto kern = decode_kernel<T, D, RB, false>;
     DL_LAUNCH_DEPENDENT(kern, P, kThreads, C::SMEM, st, mk, mv, a, w, 0, false);
   }
-  // masses: 1024 tokens a CTA, fewer while that leaves SMs idle (with two
-  // batches of loads a thread the join's first 3 us are shared; a batch's
-  // longest sequence must not take its time alone either)
+  // masses: three batches of loads a thread, which share the join's first 3 us
+  // (32 x 8K ragged, 1 / 2 / 3 batches: 63.1 / 60.9 / 60.3 us), fewer while that
+  // leaves SMs idle
   int chunks = 0;
   if (a.tok_mass && s.L_ctx > 0) {
     const int rows = s.H / a.n_mass, tj = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8;
     const int dec = s.batch * a.n_mass, idle = (4 * tc_sm_count() + dec - 1) / dec;
     const int most = (s.L_ctx + kJoinThreads * tj - 1) / (kJoinThreads * tj);
-    const int few = (s.L_ctx + 1023) / 1024;
+    const int few = (s.L_ctx + 3 * kJoinThreads * tj - 1) / (3 * kJoinThreads * tj);
     chunks = idle > few ? idle : few;
     chunks = chunks < most ? chunks : most;
     chunks = chunks < 4096 ? chunks : 4096;
