@@ -25,9 +25,11 @@
 // Rows too long for the cluster's shared memory go through it in tiles, read
 // again for every pass.
 //
-// Moves: bound by HBM (each moved row is read and written once).  A warp
-// resolves 32 moves at a time, one per lane, then all lanes copy their rows in
-// 16-byte pieces, eight loads ahead of the stores.
+// Moves: bound by HBM (each moved row is read and written once) with rows of 128
+// to 512 bytes at random places: 206 MB of them at 4.95 TB/s.  A warp resolves 32
+// moves at a time, one per lane, then all lanes copy their rows in 16-byte
+// pieces, eight loads ahead of the stores.  (Bulk copies through shared memory,
+// with 2.5 times as much in flight, took as long: 42.8 against 41.9 us.)
 #include "cluster.cuh"
 #include "common.cuh"
 #include "internal.h"
