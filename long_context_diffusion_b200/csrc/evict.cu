@@ -40,8 +40,6 @@ namespace dl {
 
 namespace {
 
-constexpr int kEvThreads = 1024;
-constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxChunks = 8;            // 16-byte chunks of a thread
 constexpr unsigned kHeldKey = 0xFF800000u;  // the key of +infinity
@@ -63,20 +61,21 @@ __device__ __forceinline__ int warp_inclusive(int v, int lane) {
   return v;
 }
 
-// CPL: 16-byte chunks (four tokens) of a thread.  VEC: masses and positions may
-// be read 16 bytes at a time.
-template <int CPL, bool VEC>
-__global__ void __launch_bounds__(kEvThreads, 1)
+// NT: threads, 512 or 1024.  CPL: 16-byte chunks (four tokens) of a thread.  VEC:
+// masses and positions may be read 16 bytes at a time.
+template <int NT, int CPL, bool VEC>
+__global__ void __launch_bounds__(NT, 1024 / NT)
 evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
+  constexpr int NW = NT / 32;            // warps
   constexpr int IT = 4 * CPL;            // tokens of a thread
   constexpr int PITCH = CPL | 1;         // chunks from lane to lane: odd, to spread the banks
   extern __shared__ uint4 s_key[];       // [thread][PITCH], later the lists
   __shared__ __align__(16) int s_hist[4096 + 2 * 1024];
   __shared__ int s_group[3][128];        // this CTA's counts of 32 bins
   __shared__ int s_gsum[128], s_bsum[32];  // the cluster's
-  __shared__ int s_wt[3][kEvWarps];      // per warp: ties, holes, fills
+  __shared__ int s_wt[3][NW];      // per warp: ties, holes, fills
   __shared__ int s_ct[4];                // this CTA's: largest position, ties, holes, fills
-  __shared__ int s_max[kEvWarps];
+  __shared__ int s_max[NW];
   const Shape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = cs > 1 ? cluster_rank() : 0;
@@ -84,7 +83,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
   pdl_trigger();
   pdl_wait();
   const int n = a.ctx_len[b];
-  for (int i = tid; i < 4096 + 2 * 1024; i += kEvThreads) s_hist[i] = 0;
+  for (int i = tid; i < 4096 + 2 * 1024; i += NT) s_hist[i] = 0;
   const bool bad = n < 0 || n > s.L_ctx;
   if (tid == 0 && rank == 0 && row % a.n_mass == 0) {
     if (bad) flag_error(a.err, ERR_BAD_INDEX);
@@ -98,7 +97,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
     const int* pos = a.tok_pos ? a.tok_pos + (size_t)row * s.L_ctx : nullptr;
     const unsigned len = (unsigned)n;
     // this warp's first token of tile k (unsigned: the last may lie past 2^31)
-    auto warp_at = [&](int k) { return (unsigned)((rank * tiles + k) * kEvWarps + warp) * (32u * IT); };
+    auto warp_at = [&](int k) { return (unsigned)((rank * tiles + k) * NW + warp) * (32u * IT); };
     // four values from token t on; behind the row's end, its last ones
     auto load4 = [&](const int* x, unsigned t) -> int4 {
       if (VEC) return *reinterpret_cast<const int4*>(x + min(t, (len - 1u) & ~3u));
@@ -147,7 +146,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
     last = __reduce_max_sync(0xffffffffu, last);
     if (lane == 0) s_max[warp] = last;
     __syncthreads();
-    last = __reduce_max_sync(0xffffffffu, s_max[lane]);
+    last = __reduce_max_sync(0xffffffffu, s_max[lane % NW]);
     if (cs > 1) {
       if (tid == 0) s_ct[0] = last;
       cluster_sync();
@@ -225,20 +224,20 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
         }
       }
       __syncthreads();
-      if (tid < groups * 8) {            // eight lanes a group
-        const int4 v = reinterpret_cast<const int4*>(hist)[tid];
+      for (int e = tid; e < groups * 8; e += NT) {  // eight lanes a group
+        const int4 v = reinterpret_cast<const int4*>(hist)[e];
         int c = (v.x + v.y) + (v.z + v.w);
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-        if ((lane & 7) == 0) s_group[pass][tid >> 3] = c;
+        if ((lane & 7) == 0) s_group[pass][e >> 3] = c;
       }
       if (cs > 1) cluster_sync(); else __syncthreads();
       if (cs > 1) {
-        if (tid < groups * 8) {          // lane & 7 = rank
-          int c = (lane & 7) < cs ? peer_int(&s_group[pass][tid >> 3], lane & 7) : 0;
+        for (int e = tid; e < groups * 8; e += NT) {  // lane & 7 = rank
+          int c = (lane & 7) < cs ? peer_int(&s_group[pass][e >> 3], lane & 7) : 0;
 #pragma unroll
           for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-          if ((lane & 7) == 0) s_gsum[tid >> 3] = c;
+          if ((lane & 7) == 0) s_gsum[e >> 3] = c;
         }
         __syncthreads();
       }
@@ -303,7 +302,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
       ties = __reduce_add_sync(0xffffffffu, ties);
       if (lane == 0) s_wt[0][warp] = ties;
       __syncthreads();
-      const int all = __reduce_add_sync(0xffffffffu, s_wt[0][lane]);
+      const int all = __reduce_add_sync(0xffffffffu, lane < NW ? s_wt[0][lane] : 0);
       if (tid == 0) s_ct[1] = all;
       cluster_sync();
       tie_first = __reduce_add_sync(0xffffffffu, lane < rank ? peer_int(&s_ct[1], lane) : 0);
@@ -319,7 +318,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
       __syncthreads();                   // the last counts are no longer read
       if (lane == 31) s_wt[0][warp] = upto;
       __syncthreads();
-      const int t = s_wt[0][lane];
+      const int t = lane < NW ? s_wt[0][lane] : 0;
       const int before = seen + __reduce_add_sync(0xffffffffu, lane < warp ? t : 0) + upto - c;
       seen += __reduce_add_sync(0xffffffffu, t);
       const int stay = min(c, max(0, want - before));
@@ -347,8 +346,8 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
       const int h = __reduce_add_sync(0xffffffffu, holes), f = __reduce_add_sync(0xffffffffu, fills);
       if (lane == 0) { s_wt[1][warp] = h; s_wt[2][warp] = f; }
       __syncthreads();
-      const int all_h = __reduce_add_sync(0xffffffffu, s_wt[1][lane]);
-      const int all_f = __reduce_add_sync(0xffffffffu, s_wt[2][lane]);
+      const int all_h = __reduce_add_sync(0xffffffffu, lane < NW ? s_wt[1][lane] : 0);
+      const int all_f = __reduce_add_sync(0xffffffffu, lane < NW ? s_wt[2][lane] : 0);
       if (tid == 0) { s_ct[2] = all_h; s_ct[3] = all_f; }
       cluster_sync();
       const int pf = lane < cs ? peer_int(&s_ct[3], lane) : 0;
@@ -368,7 +367,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
       __syncthreads();                   // keys and the last counts are no longer read
       if (lane == 31) s_wt[1][warp] = upto;
       __syncthreads();
-      const int t = s_wt[1][lane];       // at most 2^15 of each: no carry
+      const int t = lane < NW ? s_wt[1][lane] : 0;  // at most 2^15 of each: no carry
       const unsigned before = (unsigned)(__reduce_add_sync(0xffffffffu, lane < warp ? (unsigned)t : 0u) + upto - both);
       const unsigned all = __reduce_add_sync(0xffffffffu, (unsigned)t);
       const int nh = all & 0xffffu, nf = all >> 16;
@@ -376,8 +375,8 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
       for (int at = before & 0xffffu; hw; hw &= hw - 1) list[at++] = t0 + __ffs(hw) - 1;
       for (int at = nh + (before >> 16); fw; fw &= fw - 1) list[at++] = t0 + __ffs(fw) - 1;
       __syncthreads();
-      for (int i = tid; i < nh; i += kEvThreads) hole[hole_first + i] = list[i];
-      for (int i = tid; i < nf; i += kEvThreads) fill[fill_first + i] = list[nh + i];
+      for (int i = tid; i < nh; i += NT) hole[hole_first + i] = list[i];
+      for (int i = tid; i < nf; i += NT) fill[fill_first + i] = list[nh + i];
       hole_first += nh;
       fill_first += nf;
       if (tiles > 1) __syncthreads();
@@ -385,7 +384,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int tiles) {
     if (cs == 1) moves = fill_first;
     if (cs > 1) cluster_sync();          // no CTA leaves while its counts are read
   }
-  for (int i = moves + rank * kEvThreads + tid; i < a.max_move; i += cs * kEvThreads)
+  for (int i = moves + rank * NT + tid; i < a.max_move; i += cs * NT)
     hole[i] = fill[i] = -1;
   if (tid == 0 && rank == 0) a.move_cnt[row] = moves;
 }
@@ -459,14 +458,14 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, int groups, long lon
   }
 }
 
-template <int CPL, bool VEC>
+template <int NT, int CPL, bool VEC>
 cudaError_t run_evict(const EvictArgs& a, int cs, int tiles, cudaStream_t st) {
-  constexpr int kSmem = (CPL | 1) * 16 * kEvThreads;
-  cudaError_t e = allow_smem<evict_select_kernel<CPL, VEC>>(kSmem);
+  constexpr int kSmem = (CPL | 1) * 16 * NT;
+  cudaError_t e = allow_smem<evict_select_kernel<NT, CPL, VEC>>(kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.s.batch * a.n_mass) * cs);
-  cfg.blockDim = dim3(kEvThreads);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -475,32 +474,37 @@ cudaError_t run_evict(const EvictArgs& a, int cs, int tiles, cudaStream_t st) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<CPL, VEC>, a, cs, tiles);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<NT, CPL, VEC>, a, cs, tiles);
 }
 
-template <bool VEC>
-cudaError_t run_evict(const EvictArgs& a, int cs, long long chunks, cudaStream_t st) {
-  if (chunks <= 1) return run_evict<1, VEC>(a, cs, 1, st);
-  if (chunks <= 2) return run_evict<2, VEC>(a, cs, 1, st);
-  if (chunks <= 4) return run_evict<4, VEC>(a, cs, 1, st);
-  return run_evict<kMaxChunks, VEC>(a, cs, (int)((chunks + kMaxChunks - 1) / kMaxChunks), st);
+template <int NT, bool VEC>
+cudaError_t run_evict(const EvictArgs& a, cudaStream_t st) {
+  // As many CTAs a row as keep one per SM, at least one chunk a thread; longer
+  // rows take more, up to the cluster's eight.
+  const long long rows = (long long)a.s.batch * a.n_mass, L = a.s.L_ctx;
+  int cs = 1;
+  while (cs < kMaxCluster && ((rows * cs * 2 <= tc_sm_count() && L > 4ll * cs * NT) ||
+                              L > 4ll * cs * kMaxChunks * NT))
+    cs *= 2;
+  const long long chunks = (L + 4ll * cs * NT - 1) / (4ll * cs * NT);
+  if (chunks <= 1) return run_evict<NT, 1, VEC>(a, cs, 1, st);
+  if (chunks <= 2) return run_evict<NT, 2, VEC>(a, cs, 1, st);
+  if (chunks <= 4) return run_evict<NT, 4, VEC>(a, cs, 1, st);
+  return run_evict<NT, kMaxChunks, VEC>(a, cs, (int)((chunks + kMaxChunks - 1) / kMaxChunks), st);
 }
 
 }  // namespace
 
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st) {
-  // As many CTAs a row as keep one per SM, at least one chunk a thread; longer
-  // rows take more, up to the cluster's eight.
-  const long long rows = (long long)a.s.batch * a.n_mass, L = a.s.L_ctx;
-  const int sms = tc_sm_count();
-  int cs = 1;
-  while (cs < kMaxCluster && ((rows * cs * 2 <= sms && L > 4ll * cs * kEvThreads) ||
-                              L > 4ll * cs * kMaxChunks * kEvThreads))
-    cs *= 2;
-  const long long chunks = (L + 4ll * cs * kEvThreads - 1) / (4ll * cs * kEvThreads);
-  const bool vec = L % 4 == 0 && (reinterpret_cast<uintptr_t>(a.tok_mass) & 15) == 0 &&
+  const bool vec = a.s.L_ctx % 4 == 0 && (reinterpret_cast<uintptr_t>(a.tok_mass) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(a.tok_pos) & 15) == 0;
-  return vec ? run_evict<true>(a, cs, chunks, st) : run_evict<false>(a, cs, chunks, st);
+  // 1024 threads a row, one CTA per SM.  Rows in more than one wave of those take
+  // 512, two per SM, while one CTA holds a row (512 rows of 2112 tokens 24.3 ->
+  // 14.2 us, of 8192 36.1 -> 25.6, of 16384 49.0 -> 40.4; of 32768, in clusters of
+  // two, 72.3 -> 86.6; 128 rows of 2112 6.7 -> 7.6).
+  if ((long long)a.s.batch * a.n_mass > tc_sm_count() && a.s.L_ctx <= 4 * kMaxChunks * 512)
+    return vec ? run_evict<512, true>(a, st) : run_evict<512, false>(a, st);
+  return vec ? run_evict<1024, true>(a, st) : run_evict<1024, false>(a, st);
 }
 
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {

@@ -407,6 +407,8 @@ EVICT_CASES = [
     (400000, [400000], 1, 90000, 0, 0, False, "ties"),
     (300001, [300001], 1, 150000, 0, 9, True, "ties"),                  # 37 iterations a warp
     (1500, [1500] * 90 + [900, 1200], 2, 800, 2, 16, False, "random"),  # more rows than SMs
+    (9001, [9001, 8999] * 40, 2, 3000, 1, 8, False, "ties"),
+    (17000, [17000, 16000] * 40, 2, 1000, 0, 50, True, "random"),
 ]
 
 
