@@ -456,14 +456,20 @@ cudaError_t run_rope(const RopeArgs& a, cudaStream_t st) {
   const Shape& s = a.s;
   constexpr int RPP = kRopeThreads / (D / 8);
   const int n_rows = s.H + 2 * s.H_kv;
-  // Eight tokens a CTA when a sequence has them.  Rows are split over CTAs down
-  // to one pass each while that is needed to fill the GPU six CTAs deep.
-  const int tt = a.n_tok >= 8 ? 8 : 1;
+  // Tokens a CTA: eight when a sequence has them; 32 where a token has few rows
+  // and there are enough (3 rows of 64, 138 K tokens: 66.6 us at 8, 43.0 at 32;
+  // 3000 tokens: 5.5 at 8, 8.5 at 32).  Rows are split over CTAs down to one pass
+  // each while that is needed to fill the GPU six CTAs deep.
+  const int sms = tc_sm_count();
+  const bool few = n_rows < 20;
+  const int tt = few && (long long)s.batch * (a.n_tok / 32) >= 4ll * sms ? 32 : a.n_tok >= 8 ? 8 : 1;
   const int tiles = (a.n_tok + tt - 1) / tt;
-  const long long all = (long long)s.batch * tiles, want = 6ll * tc_sm_count();
-  // Enough tokens to fill the GPU without splitting their rows, and runs of
-  // eight columns that are rotated or left alone as a whole.
-  if (tt == 8 && all >= 2ll * tc_sm_count() && a.rot_dim % 16 == 0) {
+  const long long all = (long long)s.batch * tiles, want = 6ll * sms;
+  // The long-prompt kernel: enough tokens to fill the GPU without splitting their
+  // rows, enough rows to share the coefficients (24 rows: 65.5 against 70.4 us, 12
+  // rows: 70.8 against 53.5), and runs of eight columns that are rotated or left
+  // alone as a whole.
+  if (tt == 8 && !few && all >= 2ll * sms && a.rot_dim % 16 == 0) {
     if (a.interleaved)
       DL_LAUNCH_DEPENDENT((qk_norm_rope_wide_kernel<T, D, true>), (unsigned)all, kWideThreads, 0, st, a, tiles);
     else
@@ -475,7 +481,9 @@ cudaError_t run_rope(const RopeArgs& a, cudaStream_t st) {
   split = split < most ? split : most;
   const int per = (n_rows + (int)split - 1) / (int)split;
   const dim3 grid((unsigned)all, (n_rows + per - 1) / per);
-  if (tt == 1) {
+  if (tt == 32) {
+    DL_LAUNCH_DEPENDENT((qk_norm_rope_kernel<T, D, 32, 4>), grid, kRopeThreads, 0, st, a, tiles, per);
+  } else if (tt == 1) {
     DL_LAUNCH_DEPENDENT((qk_norm_rope_kernel<T, D, 1, 1>), grid, kRopeThreads, 0, st, a, tiles, per);
   } else if (per * tt <= RPP) {
     DL_LAUNCH_DEPENDENT((qk_norm_rope_kernel<T, D, 8, 1>), grid, kRopeThreads, 0, st, a, tiles, per);
