@@ -96,6 +96,10 @@ ROPE_CASES = [
     ("bf16", 128, 2, 1, 2404, 1, 40, True, False, 0),    # 40: by fours
     ("fp32", 128, 3, 1, 1201, 2, 128, True, True, 4),
     ("fp32", 64, 4, 2, 2369, 1, 64, False, False, 0),
+    # many tokens of few rows
+    ("bf16", 64, 1, 1, 6400, 3, 64, True, False, 0),
+    ("bf16", 128, 4, 2, 9500, 2, 24, False, True, 0),
+    ("bf16", 128, 20, 2, 1200, 2, 128, True, False, 0),
 ]
 
 
@@ -269,6 +273,8 @@ DECODE_CASES = [
     ("fp32", 64, 9, 1, 2100, [2100, 64], 1, 1.0),
     ("fp32", 128, 2, 3, 3000, [2999], 3, 1.0),
     ("bf16", 64, 1, 5, 150, [150, 20, 0] * 12, 5, 1.0),  # clusters of one CTA
+    ("bf16", 64, 16, 8, 130, [130, 1, 0, 64] * 10, 8, 1.0),  # more query rows than the join takes at once
+    ("fp32", 64, 4, 16, 3, [3, 0, 1] * 9, 1, 0.5),
 ]
 
 
