@@ -21,6 +21,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "sm100.cuh"
 #include "tc_common.cuh"
 
 namespace dl {
@@ -214,12 +215,16 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int tiles, int rows_per_
 //
 // With the kernel above the instructions, not HBM, set the time of a prompt
 // (176 for two rows of a warp, 62 of 91 us).  Here a thread holds two runs of
-// eight columns (off0.. and off1.., 16-byte loads) of one token and walks the
-// heads, so that the row's coefficients stay in registers with the norm's
-// weights multiplied in,
+// eight columns (off0.. and off1..) of one token and walks the heads, so that
+// the row's coefficients stay in registers with the norm's weights multiplied in,
 //   y_u' = inv (x_u (w_u cos) - x_v (w_v sin)),
 //   y_v' = inv (x_v (w_v cos) + x_u (w_u sin)),
-// and pairs of columns share an instruction (f32x2).
+// and pairs of columns share an instruction (f32x2).  Rows under way stand in a
+// ring of shared memory: asynchronous copies of 16 bytes into slots of the thread
+// that reads them, so that no thread waits for another, across the kinds of heads.
+// 8192 tokens of 96 rows (405 MB): 69.6 us, 5.8 TB/s; 65536: 515 us, 6.3 TB/s.
+// With rows loaded ahead into registers 74.5 and 542; two, six and eight rows
+// under way 75.1, 69.9 and 70.2; five CTAs per SM 73.9.
 __device__ __forceinline__ unsigned long long pack2(float x, float y) {
   unsigned long long r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
@@ -242,11 +247,25 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigne
   return r;
 }
 
-// Eight consecutive values as loaded.
+constexpr int kWideTokens = 8, kWideThreads = 128;
+
+// 16 bytes into shared memory.  Of fp32 rows a thread's pieces are halves of a
+// sector, so they pass L1 (139 us at 8192 tokens of 96 rows, 195 beside it).
+template <typename T>
+__device__ __forceinline__ void copy16(uint32_t dst, const T* src) {
+  if (sizeof(T) == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Eight consecutive values as loaded.  take(): from a thread's slots of the ring.
 template <typename T> struct Oct;
 template <> struct Oct<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void take(uint32_t slot) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(slot) : "memory");
+  }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
   __device__ __forceinline__ void get(unsigned long long (&x)[4]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -270,6 +289,13 @@ template <> struct Oct<float> {
     v[0] = *reinterpret_cast<const float4*>(p);
     v[1] = *reinterpret_cast<const float4*>(p + 4);
   }
+  __device__ __forceinline__ void take(uint32_t slot) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[i].x), "=f"(v[i].y), "=f"(v[i].z), "=f"(v[i].w)
+                   : "r"(slot + i * kWideThreads * 16) : "memory");
+  }
   __device__ __forceinline__ void store(float* p) const {
     *reinterpret_cast<float4*>(p) = v[0];
     *reinterpret_cast<float4*>(p + 4) = v[1];
@@ -290,14 +316,14 @@ template <> struct Oct<float> {
   }
 };
 
-constexpr int kWideTokens = 8, kWideThreads = 128;
-
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kWideThreads, 4)
 qk_norm_rope_wide_kernel(const __grid_constant__ RopeArgs a, int tiles) {
   constexpr int TT = kWideTokens, TPR = D / 16;       // threads per row
   constexpr int GR = kWideThreads / (TT * TPR);       // heads taken at a time
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;           // rows loaded ahead
+  constexpr int V = (int)sizeof(T);                   // 16-byte pieces of a thread's columns of a row
+  constexpr int S = 8 / (int)sizeof(T);               // rows under way
+  __shared__ __align__(16) char s_ring[S * V * kWideThreads * 16];
   __shared__ float s_cos[TT][D / 2], s_sin[TT][D / 2];
   __shared__ long long s_row[TT];
   const Shape& s = a.s;
@@ -324,6 +350,21 @@ qk_norm_rope_wide_kernel(const __grid_constant__ RopeArgs a, int tiles) {
   }
   pdl_trigger();
   pdl_wait();
+  // a token past the last reads the last one's rows and writes nothing
+  const T* src = reinterpret_cast<const T*>(a.qkv) + (tok0 + min(t, n_tok - 1)) * a.qkv_stride;
+  const int rows = s.H + 2 * s.H_kv;                  // query, key, value heads, side by side
+  const uint32_t slot0 = sm100::smem_u32(s_ring) + tid * 16;
+  auto fetch = [&](int slot, int r) {
+    if (r < rows) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        copy16<T>(slot0 + (slot * V + i) * kWideThreads * 16,
+                  src + (size_t)r * D + (i < V / 2 ? off0 : off1) + i % (V / 2) * (16 / (int)sizeof(T)));
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int u = 0; u < S; ++u) fetch(u, grp + u * GR);
   for (int e = tid; e < n_tok * half; e += kWideThreads) {
     const int tt = e / half, j = e - tt * half;
     turn(a, tok0 + tt, j, &s_sin[tt][j], &s_cos[tt][j]);
@@ -331,124 +372,118 @@ qk_norm_rope_wide_kernel(const __grid_constant__ RopeArgs a, int tiles) {
   if (tid < n_tok) s_row[tid] = cache_row(a, b, i0 + tid, true);
   __syncthreads();
   const long long row = live ? s_row[t] : -1;
-  // a token past the last reads the last one's rows and writes nothing
-  const T* src = reinterpret_cast<const T*>(a.qkv) + (tok0 + min(t, n_tok - 1)) * a.qkv_stride;
+  int kind = 0, last = 0, slot = 0;
+  T *out = nullptr, *pool = nullptr;
+  bool scaled = false;
+  unsigned long long A[4], B[4], C[4], E[4];
 #pragma unroll 1
-  for (int kind = 0; kind < 3; ++kind) {              // query, key, value heads
-    const int n = kind == 0 ? s.H : s.H_kv;
-    const int h0 = kind == 0 ? 0 : kind == 1 ? s.H : s.H + s.H_kv;
-    T* out = reinterpret_cast<T*>(kind == 0 ? a.Q_out : kind == 1 ? a.K_out : a.V_out);
-    if (out) out += ((size_t)b * n * a.n_tok + i0 + t) * D;
-    T* pool = nullptr;
-    if (kind > 0 && row >= 0) pool = reinterpret_cast<T*>(kind == 1 ? a.K_pool : a.V_pool) + row * D;
-    const T* x0 = src + (size_t)h0 * D;
-    const T* w = reinterpret_cast<const T*>(kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr);
-    // coefficients of the two runs: out0 = x0 A + other B, out1 = x1 C + other D
-    unsigned long long A[4], B[4], C[4], E[4];
-    if (kind < 2) {
-      unsigned long long w0[4], w1[4];
+  for (int r = grp; r < rows; r += GR) {  // uniform over a warp
+    if (r >= last) {                                  // the first row of a kind
+      kind = r < s.H ? 0 : r < s.H + s.H_kv ? 1 : 2;
+      const int n = kind == 0 ? s.H : s.H_kv;
+      const int h0 = kind == 0 ? 0 : kind == 1 ? s.H : s.H + s.H_kv;
+      last = h0 + n;
+      out = reinterpret_cast<T*>(kind == 0 ? a.Q_out : kind == 1 ? a.K_out : a.V_out);
+      if (out) out += ((size_t)b * n * a.n_tok + i0 + t + (long long)(r - h0) * a.n_tok) * D;
+      pool = nullptr;
+      if (kind > 0 && row >= 0)
+        pool = reinterpret_cast<T*>(kind == 1 ? a.K_pool : a.V_pool) + (row + (long long)(r - h0) * 64) * D;
+      const T* w = reinterpret_cast<const T*>(kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr);
+      scaled = w != nullptr;
+      if (kind < 2) {
+        unsigned long long w0[4], w1[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w0[i] = w1[i] = pack2(1.0f, 1.0f);
-      if (w) {
-        Oct<T> o;
-        o.load(w + off0);
-        o.get(w0);
-        o.load(w + off1);
-        o.get(w1);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 p = unpack2(w0[i]), q = unpack2(w1[i]);
-        float c0 = 1.0f, c1 = 1.0f, c2 = 1.0f, c3 = 1.0f, s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-        if (rotated && live) {
-          if (INTER) {                                // pair i of each run
-            c0 = c1 = s_cos[t][8 * c + i]; s0 = s1 = s_sin[t][8 * c + i];
-            c2 = c3 = s_cos[t][8 * c + 4 + i]; s2 = s3 = s_sin[t][8 * c + 4 + i];
-          } else {
-            c0 = c2 = s_cos[t][8 * c + 2 * i]; s0 = s2 = s_sin[t][8 * c + 2 * i];
-            c1 = c3 = s_cos[t][8 * c + 2 * i + 1]; s1 = s3 = s_sin[t][8 * c + 2 * i + 1];
-          }
+        for (int i = 0; i < 4; ++i) w0[i] = w1[i] = pack2(1.0f, 1.0f);
+        if (w) {
+          Oct<T> o;
+          o.load(w + off0);
+          o.get(w0);
+          o.load(w + off1);
+          o.get(w1);
         }
-        A[i] = pack2(p.x * c0, p.y * c1);
-        C[i] = pack2(q.x * c2, q.y * c3);
-        // what the partner adds: its own weight, minus for the first of a pair
-        B[i] = INTER ? pack2(-p.y * s0, p.x * s1) : pack2(-q.x * s0, -q.y * s1);
-        E[i] = INTER ? pack2(-q.y * s2, q.x * s3) : pack2(p.x * s2, p.y * s3);
-      }
-    }
-    Oct<T> v0[U], v1[U];                              // rows under way: a rolling window
-    auto fetch = [&](int u, int h) {
-      const T* x = x0 + (size_t)min(h, n - 1) * D;
-      v0[u].load(x + off0);
-      v1[u].load(x + off1);
-    };
 #pragma unroll
-    for (int u = 0; u < U; ++u) fetch(u, grp + u * GR);
-#pragma unroll 1
-    for (int r = grp; r - grp < n; r += U * GR) {  // uniform over the CTA
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (kind < 2) {
-          unsigned long long x[4], y[4];
-          v0[u].get(x);
-          v1[u].get(y);
-          unsigned long long inv = pack2(1.0f, 1.0f);
-          if (w) {
-            unsigned long long sq = mul2(x[0], x[0]);
-#pragma unroll
-            for (int i = 1; i < 4; ++i) sq = fma2(x[i], x[i], sq);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sq = fma2(y[i], y[i], sq);
-            const float2 f = unpack2(sq);
-            float q = f.x + f.y;
-#pragma unroll
-            for (int o = TPR / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-            const float z = __frsqrt_rn(q * (1.0f / D) + a.eps);
-            inv = pack2(z, z);
-          }
-          unsigned long long p[4], q[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            p[i] = mul2(x[i], A[i]);
-            q[i] = mul2(y[i], C[i]);
-          }
-          if (rotated) {                              // else the partner's values must not reach it
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (INTER) {
-                const float2 f = unpack2(x[i]), g = unpack2(y[i]);
-                p[i] = fma2(pack2(f.y, f.x), B[i], p[i]);
-                q[i] = fma2(pack2(g.y, g.x), E[i], q[i]);
-              } else {
-                p[i] = fma2(y[i], B[i], p[i]);
-                q[i] = fma2(x[i], E[i], q[i]);
-              }
+        for (int i = 0; i < 4; ++i) {
+          const float2 p = unpack2(w0[i]), q = unpack2(w1[i]);
+          float c0 = 1.0f, c1 = 1.0f, c2 = 1.0f, c3 = 1.0f, s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+          if (rotated && live) {
+            if (INTER) {                                // pair i of each run
+              c0 = c1 = s_cos[t][8 * c + i]; s0 = s1 = s_sin[t][8 * c + i];
+              c2 = c3 = s_cos[t][8 * c + 4 + i]; s2 = s3 = s_sin[t][8 * c + 4 + i];
+            } else {
+              c0 = c2 = s_cos[t][8 * c + 2 * i]; s0 = s2 = s_sin[t][8 * c + 2 * i];
+              c1 = c3 = s_cos[t][8 * c + 2 * i + 1]; s1 = s3 = s_sin[t][8 * c + 2 * i + 1];
             }
           }
-          if (w) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { p[i] = mul2(p[i], inv); q[i] = mul2(q[i], inv); }
-          }
-          v0[u].set(p);
-          v1[u].set(q);
+          A[i] = pack2(p.x * c0, p.y * c1);
+          C[i] = pack2(q.x * c2, q.y * c3);
+          // what the partner adds: its own weight, minus for the first of a pair
+          B[i] = INTER ? pack2(-p.y * s0, p.x * s1) : pack2(-q.x * s0, -q.y * s1);
+          E[i] = INTER ? pack2(-q.y * s2, q.x * s3) : pack2(p.x * s2, p.y * s3);
         }
-        const int h = r + u * GR;
-        if (h < n && live) {
-          if (out) {
-            T* o = out + (size_t)h * a.n_tok * D;
-            v0[u].store(o + off0);
-            v1[u].store(o + off1);
-          }
-          if (pool) {
-            T* o = pool + (size_t)h * 64 * D;
-            v0[u].store(o + off0);
-            v1[u].store(o + off1);
-          }
-        }
-        fetch(u, h + U * GR);
       }
     }
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    Oct<T> v0, v1;
+    v0.take(slot0 + slot * V * kWideThreads * 16);
+    v1.take(slot0 + (slot * V + V / 2) * kWideThreads * 16);
+    fetch(slot, r + S * GR);
+    slot = slot + 1 < S ? slot + 1 : 0;
+    if (kind < 2) {
+      unsigned long long x[4], y[4];
+      v0.get(x);
+      v1.get(y);
+      unsigned long long inv = pack2(1.0f, 1.0f);
+      if (scaled) {
+        unsigned long long sq = mul2(x[0], x[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) sq = fma2(x[i], x[i], sq);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sq = fma2(y[i], y[i], sq);
+        const float2 f = unpack2(sq);
+        float q = f.x + f.y;
+#pragma unroll
+        for (int o = TPR / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+        const float z = __frsqrt_rn(q * (1.0f / D) + a.eps);
+        inv = pack2(z, z);
+      }
+      unsigned long long p[4], q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = mul2(x[i], A[i]);
+        q[i] = mul2(y[i], C[i]);
+      }
+      if (rotated) {                                  // else the partner's values must not reach it
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (INTER) {
+            const float2 f = unpack2(x[i]), g = unpack2(y[i]);
+            p[i] = fma2(pack2(f.y, f.x), B[i], p[i]);
+            q[i] = fma2(pack2(g.y, g.x), E[i], q[i]);
+          } else {
+            p[i] = fma2(y[i], B[i], p[i]);
+            q[i] = fma2(x[i], E[i], q[i]);
+          }
+        }
+      }
+      if (scaled) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { p[i] = mul2(p[i], inv); q[i] = mul2(q[i], inv); }
+      }
+      v0.set(p);
+      v1.set(q);
+    }
+    if (live && out) {
+      v0.store(out + off0);
+      v1.store(out + off1);
+    }
+    if (pool) {
+      v0.store(pool + off0);
+      v1.store(pool + off1);
+      pool += (size_t)GR * 64 * D;
+    }
+    if (out) out += (size_t)GR * a.n_tok * D;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <typename T, int D>
@@ -461,15 +496,20 @@ cudaError_t run_rope(const RopeArgs& a, cudaStream_t st) {
   // 3000 tokens: 5.5 at 8, 8.5 at 32).  Rows are split over CTAs down to one pass
   // each while that is needed to fill the GPU six CTAs deep.
   const int sms = tc_sm_count();
-  const bool few = n_rows < 20;
+  const bool few = n_rows * D < 1280;
   const int tt = few && (long long)s.batch * (a.n_tok / 32) >= 4ll * sms ? 32 : a.n_tok >= 8 ? 8 : 1;
   const int tiles = (a.n_tok + tt - 1) / tt;
   const long long all = (long long)s.batch * tiles, want = 6ll * sms;
-  // The long-prompt kernel: enough tokens to fill the GPU without splitting their
-  // rows, enough rows to share the coefficients (24 rows: 65.5 against 70.4 us, 12
-  // rows: 70.8 against 53.5), and runs of eight columns that are rotated or left
-  // alone as a whole.
-  if (tt == 8 && !few && all >= 2ll * sms && a.rot_dim % 16 == 0) {
+  // The long-prompt kernel, where
+  // - the tokens fill the GPU without splitting their rows (96 rows of bf16: 1800
+  //   tokens 29.8 against 25.0 us, 2400: 30.6 against 31.6, 8192: 69 against 90;
+  //   fp32: 2400 tokens 61.4 against 50.6, 3600: 73.5 against 74.8, 8192: 135
+  //   against 159);
+  // - a token has the rows to share the coefficients (60000 tokens: 8 rows 78.6
+  //   against 69.3 us, 10: 83.2 against 84.0, 16: 106 against 124; of 64 columns,
+  //   12: 69.9 against 50.7);
+  // - runs of eight columns are rotated or left alone as a whole.
+  if (tt == 8 && !few && all >= (sizeof(T) == 2 ? 2ll : 3ll) * sms && a.rot_dim % 16 == 0) {
     if (a.interleaved)
       DL_LAUNCH_DEPENDENT((qk_norm_rope_wide_kernel<T, D, true>), (unsigned)all, kWideThreads, 0, st, a, tiles);
     else

@@ -100,6 +100,15 @@ ROPE_CASES = [
     ("bf16", 64, 1, 1, 6400, 3, 64, True, False, 0),
     ("bf16", 128, 4, 2, 9500, 2, 24, False, True, 0),
     ("bf16", 128, 20, 2, 1200, 2, 128, True, False, 0),
+    # enough tokens and rows for the long-prompt kernel; rows that its groups of
+    # two (128 columns) or four (64) do not divide, kinds shorter than a group
+    ("bf16", 128, 10, 1, 1203, 2, 128, True, False, 0),
+    ("bf16", 64, 20, 1, 803, 3, 32, True, False, 8),
+    ("bf16", 128, 9, 3, 2373, 1, 96, False, True, 0),
+    ("bf16", 64, 22, 1, 2401, 1, 0, True, False, 0),
+    ("bf16", 128, 11, 1, 2404, 1, 40, True, False, 0),   # 40: by fours
+    ("fp32", 128, 9, 3, 1803, 2, 128, True, True, 4),
+    ("fp32", 64, 18, 2, 1203, 3, 64, False, False, 0),
 ]
 
 
