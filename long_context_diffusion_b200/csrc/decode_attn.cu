@@ -1172,7 +1172,7 @@ cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
   // finished by their runs (32 sequences x 512 heads, lengths up to 64: the call
   // takes 43.4 us with a row a CTA, 25.4 with eight)
   const int all_rows = s.batch * s.H, once = 8 * tc_sm_count();
-  const int rpc = (all_rows + once - 1) / once < 8 ? (all_rows + once - 1) / once : 8;
+  const int rpc = (all_rows + once - 1) / once < 8 ? (all_rows + once - 1) / once : 8;  // 8: a warp each
   DL_LAUNCH_DEPENDENT(join, (all_rows + rpc - 1) / rpc + s.batch * a.n_mass * chunks, kJoinThreads, 0, st, a, w, RB,
                       chunks, rpc);
   return cudaGetLastError();
