@@ -34,12 +34,15 @@
 // high, 8-15 low), with 9-16 they take two.  The instruction is used because
 // a tile has at most 16 useful rows and the operands' conversion and traffic,
 // not the products, are what fills an SM here.
-// fp32: the same walk on the CUDA cores: lane = (key, quarter of d) for S, lane =
-// four columns for O.  The dot products are summed in fp64 and stay so until
-// the reference is subtracted: beside a sink's logit of 35 one fp32 rounding of
-// a logit is 1e-6 of its weight, as large as all other errors together.  (A
-// tile's 32 KB take 1400 cycles of an SM's share of HBM, its fp64 sums 512 with
-// eight heads.)
+// fp32: the same walk on the CUDA cores: lane = (two or four keys, eighth of d) for
+// S, lane = four columns for O.  The dot products are summed in fp64 and stay so
+// until the reference is subtracted: beside a sink's logit of 35 one fp32 rounding
+// of a logit is 1e-6 of its weight, as large as all other errors together.  Groups
+// of up to four heads reach HBM (2 x 32K, 32/8 heads of 128: 5.9 TB/s); with eight
+// the reads of Q from shared memory, the conversions and the fp64 sums take 1.6
+// times as long as HBM (270 us against 164; fp32 sums took 215).  Several keys a
+// lane share a read of Q: with one, and quarters of d, 300 us; with Q in
+// registers, every lane four columns and the sums dealt out over 32 lanes, 338.
 //
 // Weights.  With c = scale log2 e and a maximum m of the dot products x, the
 // reference is M = m c rounded once, and p = 2^(x c - M) in one fused
@@ -79,11 +82,12 @@ constexpr int kClusterTiles = 4, kClusterTilesFull = 16;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr double kLog2e = 1.4426950408889634;
 
-// Query heads per item block: 8; 16 for bf16 groups of more than 8; 2 for fp32
-// groups of at most 2 (on the CUDA cores empty rows cost as much as others).
+// Query heads per item block: 8; 16 for bf16 groups of more than 8; 4 or 2 for fp32
+// groups of at most as many (on the CUDA cores empty rows cost as much as others:
+// four heads in a block of eight 170 us, of four 88).
 __host__ __device__ inline int rows_per_block(const Shape& s) {
   if (s.dtype == DL_BF16) return s.G > 8 ? 16 : 8;
-  return s.G > 2 ? 8 : 2;
+  return s.G > 4 ? 8 : s.G > 2 ? 4 : 2;
 }
 __host__ __device__ inline int items_per_seq(const Shape& s) {
   const int rb = rows_per_block(s);
@@ -226,7 +230,10 @@ template <typename T, int D_, int RB_>
 struct Cfg {
   static constexpr int D = D_, RB = RB_;
   static constexpr bool BF16 = sizeof(T) == 2;
-  static constexpr int KT = BF16 ? 64 : 32;            // keys per tile
+  // Keys per tile, 32 KB of K and V; half of that for blocks of eight fp32 rows of
+  // 64, which 16 keys a warp would spill (32K keys: 357 us against 413; of four
+  // rows 64 keys 179, 32 keys 211).
+  static constexpr int KT = BF16 || (D == 64 && RB < 8) ? 64 : 32;
   static constexpr int BOX = KT * 128;                 // bytes of one 128-byte-wide box
   static constexpr int BOXES = D * (int)sizeof(T) / 128;
   static constexpr int HALF = BOX * BOXES;             // K (or V) of a stage
@@ -236,8 +243,8 @@ struct Cfg {
   static constexpr int COPIES = BF16 && RB == 8 ? 3 : 1;
   static constexpr int O_OFF = ST * STAGE;
   static constexpr int Q_OFF = O_OFF + COPIES * RB * D * 4;        // fp32 keys: rows of Q in fp64
-  static constexpr int P_OFF = Q_OFF + (BF16 ? 0 : RB * D * 8);    // fp32 keys: weights [warp][RB][8]
-  static constexpr int ML_OFF = P_OFF + (BF16 ? 0 : kWarps * RB * 8 * 4);
+  static constexpr int P_OFF = Q_OFF + (BF16 ? 0 : RB * D * 8);    // fp32 keys: weights [warp][RB][KT / 4]
+  static constexpr int ML_OFF = P_OFF + (BF16 ? 0 : RB * KT * 4);
   static constexpr int BAR_OFF = ML_OFF + kWarps * RB * 8;
   static constexpr int MISC_OFF = BAR_OFF + 2 * ST * 8;            // info [ST], abort
   static constexpr int SMEM = MISC_OFF + (ST + 4) * 4 + 1024;      // + alignment slack
@@ -429,14 +436,22 @@ struct StateTc {
 
 // Running state of one warp's keys of a segment, fp32: o holds columns
 // 4 (lane % (D/4)) .. + 3, of every second key when D is 64.
-template <int D, int RB>
+template <int D, int RB, int KT>
 struct StateF32 {
   static constexpr int CH = D / 4;          // 16-byte columns of a row
   static constexpr int KS = 32 / CH;        // keys taken at a time by the P V lanes
+  static constexpr int NKW = KT / kWarps;   // this warp's keys of a tile: 8 or 16
+  static constexpr int NK = NKW / 4;        // of them under one lane while S is taken
+  static constexpr int DUP = 32 / NKW;      // lanes with the same key afterwards
   float o[RB][4];
   float m[RB], l[RB];                       // l: of this lane's key
-  const double* sq;                         // Q rows in shared memory [RB][D]
-  float* sp;                                // this warp's weights [RB][8]
+  const double* sq;                         // Q rows in shared memory, see q_at
+  float* sp;                                // this warp's weights [RB][NKW]
+  // Column e of row r: pairs of a 16-byte column of K apart, so that the lanes of
+  // eight columns read 128 bytes side by side.
+  __device__ __forceinline__ static int q_at(int r, int e) {
+    return r * D + (e >> 1 & 1) * (D / 2) + (e >> 2) * 2 + (e & 1);
+  }
   __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
@@ -445,38 +460,65 @@ struct StateF32 {
     }
   }
   __device__ __forceinline__ static uint32_t chunk_at(int key, int c) {
-    return (c >> 3) * (32 * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
+    return (c >> 3) * (KT * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
   }
   __device__ __forceinline__ void tile(const char* ks, const char* vs, int warp, int lane, int valid,
                                        float c2, double c2d, double* logit, int Lp, int n_rows) {
-    const int kk = lane & 7, key = warp * 8 + kk, dq = lane >> 3;
-    double x[RB];
+    if (warp * NKW >= valid) return;        // none of this warp's keys
+    // S: lane = (NK keys 4 apart, eighth of the columns); lane bit 2 is the eighth's
+    // top bit, so that eight neighbouring lanes hit all banks
+    const int kk = lane & 3, dq = (lane & 4) | lane >> 3;
+    double y[NK][RB];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) x[r] = 0.0;
+    for (int n = 0; n < NK; ++n)
 #pragma unroll
-    for (int j = 0; j < CH / 4; ++j) {
-      const int c = 4 * j + dq;
-      const float4 k = *reinterpret_cast<const float4*>(ks + chunk_at(key, c));
-      const double k0 = k.x, k1 = k.y, k2 = k.z, k3 = k.w;
+      for (int r = 0; r < RB; ++r) y[n][r] = 0.0;
+#pragma unroll
+    for (int j = 0; j < CH / 8; ++j) {
+      const int c = 8 * j + dq;
+      double k[NK][4];
+#pragma unroll
+      for (int n = 0; n < NK; ++n) {
+        const float4 f = *reinterpret_cast<const float4*>(ks + chunk_at(warp * NKW + 4 * n + kk, c));
+        k[n][0] = f.x; k[n][1] = f.y; k[n][2] = f.z; k[n][3] = f.w;
+      }
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
-        const double2 p = *reinterpret_cast<const double2*>(sq + r * D + 4 * c);
-        const double2 q = *reinterpret_cast<const double2*>(sq + r * D + 4 * c + 2);
-        x[r] = fma(p.x, k0, fma(p.y, k1, fma(q.x, k2, fma(q.y, k3, x[r]))));
+        const double2 p = *reinterpret_cast<const double2*>(sq + q_at(r, 4 * c));
+        const double2 q = *reinterpret_cast<const double2*>(sq + q_at(r, 4 * c + 2));
+#pragma unroll
+        for (int n = 0; n < NK; ++n)
+          y[n][r] = fma(p.x, k[n][0], fma(p.y, k[n][1], fma(q.x, k[n][2], fma(q.y, k[n][3], y[n][r]))));
       }
     }
+    // the eighths' sums; a lane gives away keys while it has several
+    const int kl = 4 * (lane >> (NK == 2 ? 4 : 3)) + kk, key = warp * NKW + kl, dup = (lane >> 2) % DUP;
     const bool ok = key < valid;
     bool raise = false;
+    double x[RB];
     float top[RB];
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
-      x[r] += __shfl_xor_sync(0xffffffffu, x[r], 8);
-      x[r] += __shfl_xor_sync(0xffffffffu, x[r], 16);
-      if (!ok) x[r] = -INFINITY;
-      if (logit && dq == 0 && r < n_rows) logit[(size_t)r * Lp + key] = x[r];
-      float t = (float)x[r];
 #pragma unroll
-      for (int w = 1; w < 8; w <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, w));
+      for (int w = 16, n = NK; w >= 4; w >>= 1) {
+        if (n > 1) {
+          n /= 2;
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            const double keep = lane & w ? y[n + i][r] : y[i][r], give = lane & w ? y[i][r] : y[n + i][r];
+            y[i][r] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+          }
+        } else {
+          y[0][r] += __shfl_xor_sync(0xffffffffu, y[0][r], w);
+        }
+      }
+      x[r] = ok ? y[0][r] : -INFINITY;
+      if (logit && dup == 0 && r < n_rows) logit[(size_t)r * Lp + key] = x[r];
+      float t = (float)x[r];
+      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+      if (NK == 4) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
       top[r] = fmaxf(m[r], t);
       raise |= top[r] > m[r];
     }
@@ -491,35 +533,47 @@ struct StateF32 {
       }
     }
     __syncwarp();
+    // weights, those of one P V lane side by side
+    const int at = kl % KS * (NKW / KS) + kl / KS;
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
       const float M = m[r] == -INFINITY ? 0.0f : __fmul_rn(m[r], c2);
       const float p = ex2_approx((float)fma(x[r], c2d, -(double)M));
       l[r] += p;
-      if (dq == (r & 3)) sp[r * 8 + kk] = p;
+      if (dup == r % DUP) sp[r * NKW + at] = p;
     }
     __syncwarp();
     const int c = lane % CH, ks0 = lane / CH;
 #pragma unroll
-    for (int k = 0; k < 8; k += KS) {
-      const int kl = k + ks0;
-      float4 v = *reinterpret_cast<const float4*>(vs + chunk_at(warp * 8 + kl, c));
-      if (warp * 8 + kl >= valid) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // behind the last token
+    for (int k0 = 0; k0 < NKW / KS; k0 += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = warp * NKW + (k0 + i) * KS + ks0;
+        v[i] = *reinterpret_cast<const float4*>(vs + chunk_at(t, c));
+        if (t >= valid) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // behind the last token
+      }
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
-        const float p = sp[r * 8 + kl];
-        o[r][0] = fmaf(p, v.x, o[r][0]);
-        o[r][1] = fmaf(p, v.y, o[r][1]);
-        o[r][2] = fmaf(p, v.z, o[r][2]);
-        o[r][3] = fmaf(p, v.w, o[r][3]);
+        const float4 q = *reinterpret_cast<const float4*>(sp + r * NKW + ks0 * (NKW / KS) + k0);
+        const float p[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[r][0] = fmaf(p[i], v[i].x, o[r][0]);
+          o[r][1] = fmaf(p[i], v[i].y, o[r][1]);
+          o[r][2] = fmaf(p[i], v[i].z, o[r][2]);
+          o[r][3] = fmaf(p[i], v[i].w, o[r][3]);
+        }
       }
     }
   }
   __device__ __forceinline__ void finish(int) {
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
-#pragma unroll
-      for (int w = 1; w < 8; w <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
+      if (NK == 4) l[r] += __shfl_xor_sync(0xffffffffu, l[r], 8);
       if constexpr (KS == 2) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[r][e] += __shfl_xor_sync(0xffffffffu, o[r][e], 16);
@@ -788,7 +842,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
   }
 
   // ---- computing warps
-  using State = typename std::conditional<C::BF16, StateTc<D, RB>, StateF32<D, RB>>::type;
+  using State = typename std::conditional<C::BF16, StateTc<D, RB>, StateF32<D, RB, C::KT>>::type;
   State st8;
   float* s_o = reinterpret_cast<float*>(sm + C::O_OFF);
   float2* s_ml = reinterpret_cast<float2*>(sm + C::ML_OFF);
@@ -804,10 +858,11 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     } else {
       double* sq = reinterpret_cast<double*>(sm + C::Q_OFF);
       named_bar_sync(1, kWarps * 32);  // the last segment's rows are no longer read
-      for (int e = tid; e < RB * D; e += kWarps * 32) sq[e] = e < n_rows * D ? (double)q[e] : 0.0;
+      for (int e = tid; e < RB * D; e += kWarps * 32)
+        sq[State::q_at(e / D, e % D)] = e < n_rows * D ? (double)q[e] : 0.0;
       named_bar_sync(1, kWarps * 32);
       st8.sq = sq;
-      st8.sp = reinterpret_cast<float*>(sm + C::P_OFF) + warp * RB * 8;
+      st8.sp = reinterpret_cast<float*>(sm + C::P_OFF) + warp * RB * State::NKW;
     }
     st8.reset();
     for (int t = seg.t0; t < seg.t1; ++t, ++k) {
@@ -1182,6 +1237,17 @@ cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
 
 size_t decode_workspace(const Shape& s, bool mass) { return carve(s, mass, nullptr, nullptr); }
 
+namespace {
+
+template <int D>
+cudaError_t run_decode_f32(const DecodeArgs& a, cudaStream_t st) {
+  const int rb = rows_per_block(a.s);
+  if (rb == 8) return run_decode<float, D, 8>(a, st);
+  return rb == 4 ? run_decode<float, D, 4>(a, st) : run_decode<float, D, 2>(a, st);
+}
+
+}  // namespace
+
 cudaError_t launch_decode_attn(const DecodeArgs& a, cudaStream_t st) {
   const Shape& s = a.s;
   if (s.dtype == DL_BF16) {
@@ -1189,8 +1255,7 @@ cudaError_t launch_decode_attn(const DecodeArgs& a, cudaStream_t st) {
       return s.G > 8 ? run_decode<__nv_bfloat16, 128, 16>(a, st) : run_decode<__nv_bfloat16, 128, 8>(a, st);
     return s.G > 8 ? run_decode<__nv_bfloat16, 64, 16>(a, st) : run_decode<__nv_bfloat16, 64, 8>(a, st);
   }
-  if (s.d == 128) return s.G > 2 ? run_decode<float, 128, 8>(a, st) : run_decode<float, 128, 2>(a, st);
-  return s.G > 2 ? run_decode<float, 64, 8>(a, st) : run_decode<float, 64, 2>(a, st);
+  return s.d == 128 ? run_decode_f32<128>(a, st) : run_decode_f32<64>(a, st);
 }
 
 }  // namespace dl
