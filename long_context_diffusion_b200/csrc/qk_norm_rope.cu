@@ -332,21 +332,23 @@ qk_norm_rope_wide_kernel(const __grid_constant__ RopeArgs a, int tiles) {
   const int n_tok = min(TT, a.n_tok - i0), half = a.rot_dim / 2;
   const size_t tok0 = (size_t)b * a.n_tok + i0;
   const bool live = t < n_tok;
-  // columns: off0 .. + 7 and off1 .. + 7; rotated pairs, or columns left alone
+  // columns: off0 .. + 7 and off1 .. + 7.  Split pairing: a run and its partners, or
+  // two runs left alone; interleaved: whole pairs, side by side over the lanes
   int off0, off1;
-  bool rotated;
+  bool rot0, rot1;
   if (INTER) {
-    off0 = 16 * c;
-    off1 = off0 + 8;
-    rotated = off0 < a.rot_dim;
+    off0 = 8 * c;
+    off1 = D / 2 + off0;
+    rot0 = off0 < a.rot_dim;
+    rot1 = off1 < a.rot_dim;
   } else if (8 * c < half) {
     off0 = 8 * c;
     off1 = half + off0;
-    rotated = true;
+    rot0 = rot1 = true;
   } else {
     off0 = a.rot_dim + 8 * c - half;
     off1 = off0 + (D - a.rot_dim) / 2;
-    rotated = false;
+    rot0 = rot1 = false;
   }
   pdl_trigger();
   pdl_wait();
@@ -405,14 +407,12 @@ qk_norm_rope_wide_kernel(const __grid_constant__ RopeArgs a, int tiles) {
         for (int i = 0; i < 4; ++i) {
           const float2 p = unpack2(w0[i]), q = unpack2(w1[i]);
           float c0 = 1.0f, c1 = 1.0f, c2 = 1.0f, c3 = 1.0f, s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-          if (rotated && live) {
-            if (INTER) {                                // pair i of each run
-              c0 = c1 = s_cos[t][8 * c + i]; s0 = s1 = s_sin[t][8 * c + i];
-              c2 = c3 = s_cos[t][8 * c + 4 + i]; s2 = s3 = s_sin[t][8 * c + 4 + i];
-            } else {
-              c0 = c2 = s_cos[t][8 * c + 2 * i]; s0 = s2 = s_sin[t][8 * c + 2 * i];
-              c1 = c3 = s_cos[t][8 * c + 2 * i + 1]; s1 = s3 = s_sin[t][8 * c + 2 * i + 1];
-            }
+          if (INTER) {                                // pair i of each run
+            if (rot0 && live) { c0 = c1 = s_cos[t][4 * c + i]; s0 = s1 = s_sin[t][4 * c + i]; }
+            if (rot1 && live) { c2 = c3 = s_cos[t][D / 4 + 4 * c + i]; s2 = s3 = s_sin[t][D / 4 + 4 * c + i]; }
+          } else if (rot0 && live) {
+            c0 = c2 = s_cos[t][8 * c + 2 * i]; s0 = s2 = s_sin[t][8 * c + 2 * i];
+            c1 = c3 = s_cos[t][8 * c + 2 * i + 1]; s1 = s3 = s_sin[t][8 * c + 2 * i + 1];
           }
           A[i] = pack2(p.x * c0, p.y * c1);
           C[i] = pack2(q.x * c2, q.y * c3);
@@ -452,17 +452,27 @@ qk_norm_rope_wide_kernel(const __grid_constant__ RopeArgs a, int tiles) {
         p[i] = mul2(x[i], A[i]);
         q[i] = mul2(y[i], C[i]);
       }
-      if (rotated) {                                  // else the partner's values must not reach it
+      // where nothing is rotated the partner's values must not reach a column
+      if (INTER) {
+        if (rot0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2(x[i]);
+            p[i] = fma2(pack2(f.y, f.x), B[i], p[i]);
+          }
+        }
+        if (rot1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 g = unpack2(y[i]);
+            q[i] = fma2(pack2(g.y, g.x), E[i], q[i]);
+          }
+        }
+      } else if (rot0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (INTER) {
-            const float2 f = unpack2(x[i]), g = unpack2(y[i]);
-            p[i] = fma2(pack2(f.y, f.x), B[i], p[i]);
-            q[i] = fma2(pack2(g.y, g.x), E[i], q[i]);
-          } else {
-            p[i] = fma2(y[i], B[i], p[i]);
-            q[i] = fma2(x[i], E[i], q[i]);
-          }
+          p[i] = fma2(y[i], B[i], p[i]);
+          q[i] = fma2(x[i], E[i], q[i]);
         }
       }
       if (scaled) {
