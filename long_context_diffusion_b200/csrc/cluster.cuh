@@ -4,6 +4,10 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
+#include "launch.cuh"
+
 namespace dl {
 
 __device__ __forceinline__ int cluster_rank() {
@@ -45,6 +49,32 @@ inline cudaLaunchAttribute cluster_of(int size) {
   a.val.clusterDim.x = size;
   a.val.clusterDim.y = a.val.clusterDim.z = 1;
   return a;
+}
+
+// Clusters of `size` CTAs (2, 4 or 8) of a kernel that are resident at once: fewer
+// than its CTAs make, because a cluster lies in one GPC (148 CTAs, one per SM: 15
+// clusters of eight, 33 of four).  Asked of the runtime once per device.
+template <auto Kernel>
+int resident_clusters(int size, int threads, int smem) {
+  static std::atomic<int> known[64][3];  // count + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::atomic<int>* slot = dev < 64 ? &known[dev][size == 2 ? 0 : size == 4 ? 1 : 2] : nullptr;
+  if (slot && slot->load(std::memory_order_relaxed)) return slot->load(std::memory_order_relaxed) - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1] = {cluster_of(size)};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (allow_smem<Kernel>(smem) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (slot) slot->store(n + 1, std::memory_order_relaxed);
+  return n;
 }
 
 }  // namespace dl

@@ -1178,9 +1178,13 @@ cudaError_t run_decode(const DecodeArgs& a, cudaStream_t st) {
   if (!ok) return cudaErrorInvalidValue;
   const int tiles = (s.L_ctx + C::KT - 1) / C::KT, fit = kCtasPerSm * tc_sm_count();
   const long long items = (long long)s.batch * items_per_seq(s);
-  // Small enough for clusters?
+  // Small enough for clusters, all resident at once?  (8 heads on one, 2400 tokens,
+  // 71 clusters of four fit: 71 items 28.5 us, as runs 32.0; 72 items 36.2 and 30.0.)
   int cs = 1;
-  while (cs < kMaxCluster && cs < tiles && items * cs * 2 <= fit) cs *= 2;
+  auto all_fit = [&](int n) {
+    return items * n <= fit && items <= resident_clusters<decode_kernel<T, D, RB, true>>(n, kThreads, C::SMEM);
+  };
+  while (cs < kMaxCluster && cs < tiles && all_fit(2 * cs)) cs *= 2;
   const bool clusters = items * cs <= fit &&
                         tiles <= cs * (4 * items * cs >= 3 * fit ? kClusterTilesFull : kClusterTiles);
   const bool own_mass = !a.tok_mass || (a.n_mass == s.H_kv && s.G <= RB);

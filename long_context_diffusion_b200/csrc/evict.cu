@@ -458,9 +458,12 @@ cache_compact_kernel(const __grid_constant__ CompactArgs a, int groups, long lon
   }
 }
 
+template <int NT, int CPL>
+constexpr int evict_smem() { return (CPL | 1) * 16 * NT; }
+
 template <int NT, int CPL, bool VEC>
 cudaError_t run_evict(const EvictArgs& a, int cs, int tiles, cudaStream_t st) {
-  constexpr int kSmem = (CPL | 1) * 16 * NT;
+  constexpr int kSmem = evict_smem<NT, CPL>();
   cudaError_t e = allow_smem<evict_select_kernel<NT, CPL, VEC>>(kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -480,10 +483,16 @@ cudaError_t run_evict(const EvictArgs& a, int cs, int tiles, cudaStream_t st) {
 template <int NT, bool VEC>
 cudaError_t run_evict(const EvictArgs& a, cudaStream_t st) {
   // As many CTAs a row as keep one per SM, at least one chunk a thread; longer
-  // rows take more, up to the cluster's eight.
+  // rows take more, up to the cluster's eight.  All clusters have to be resident at
+  // once (16 rows of 17548 tokens, 15 clusters of eight fit: 22.9 us by eights, 14.0
+  // by fours; 34 rows of 30000, 33 of four fit: 23.7 by fours, 17.2 by twos).
   const long long rows = (long long)a.s.batch * a.n_mass, L = a.s.L_ctx;
+  auto fit = [&](int n) {
+    return rows * n <= tc_sm_count() &&
+           rows <= resident_clusters<evict_select_kernel<NT, kMaxChunks, VEC>>(n, NT, evict_smem<NT, kMaxChunks>());
+  };
   int cs = 1;
-  while (cs < kMaxCluster && ((rows * cs * 2 <= tc_sm_count() && L > 4ll * cs * NT) ||
+  while (cs < kMaxCluster && ((fit(cs * 2) && L > 4ll * cs * NT) ||
                               L > 4ll * cs * kMaxChunks * NT))
     cs *= 2;
   const long long chunks = (L + 4ll * cs * NT - 1) / (4ll * cs * NT);
