@@ -39,10 +39,11 @@
 // until the reference is subtracted: beside a sink's logit of 35 one fp32 rounding
 // of a logit is 1e-6 of its weight, as large as all other errors together.  Groups
 // of up to four heads reach HBM (2 x 32K, 32/8 heads of 128: 5.9 TB/s); with eight
-// the reads of Q from shared memory, the conversions and the fp64 sums take 1.6
-// times as long as HBM (270 us against 164; fp32 sums took 215).  Several keys a
-// lane share a read of Q: with one, and quarters of d, 300 us; with Q in
-// registers, every lane four columns and the sums dealt out over 32 lanes, 338.
+// (8 x 32K, 32/4 heads) it takes 270 us against 164: issue slots are 54 % busy, the
+// fp64 pipe 24 %, and eight computing warps of 168 registers per SM do not hide the
+// rest (fp32 sums took 215).  Several keys a lane share a read of Q: with one, and
+// quarters of d, 300 us; with Q in registers, every lane four columns and the sums
+// dealt out over 32 lanes, 338.
 //
 // Weights.  With c = scale log2 e and a maximum m of the dot products x, the
 // reference is M = m c rounded once, and p = 2^(x c - M) in one fused

@@ -284,6 +284,16 @@ DECODE_CASES = [
     ("bf16", 64, 1, 5, 150, [150, 20, 0] * 12, 5, 1.0),  # clusters of one CTA
     ("bf16", 64, 16, 8, 130, [130, 1, 0, 64] * 10, 8, 1.0),  # more query rows than the join takes at once
     ("fp32", 64, 4, 16, 3, [3, 0, 1] * 9, 1, 0.5),
+    # fp32 blocks of two, four and eight rows: lengths that end in each warp's keys
+    ("fp32", 64, 3, 2, 70, [15, 16, 17, 48, 49, 63, 64, 65, 70, 1], 2, 1.0),
+    ("fp32", 128, 3, 1, 100, [7, 8, 9, 24, 25, 32, 33, 96, 97], 1, 1.0),
+    ("fp32", 128, 8, 1, 300, [300, 8, 9], 1, 1.0),
+    ("fp32", 64, 4, 3, 7000, [7000, 4097], 1, 0.7),
+    ("fp32", 128, 4, 2, 5100, [5100, 31, 33], 2, 1.0),
+    ("fp32", 64, 2, 2, 6000, [6000, 17], 2, 1.0),
+    # more items than clusters of eight (of four) that are resident at once
+    ("bf16", 128, 8, 4, 520, [520, 100, 0] * 3, 4, 1.0),
+    ("bf16", 64, 5, 4, 900, [900, 450] * 9, 1, 1.0),
 ]
 
 
@@ -424,6 +434,9 @@ EVICT_CASES = [
     (1500, [1500] * 90 + [900, 1200], 2, 800, 2, 16, False, "random"),  # more rows than SMs
     (9001, [9001, 8999] * 40, 2, 3000, 1, 8, False, "ties"),
     (17000, [17000, 16000] * 40, 2, 1000, 0, 50, True, "random"),
+    # more rows than clusters of eight (of four) that are resident at once
+    (17001, [17001, 17000], 8, 900, 4, 100, True, "random"),
+    (18000, [18000, 17000], 17, 9000, 0, 0, False, "ties"),
 ]
 
 
