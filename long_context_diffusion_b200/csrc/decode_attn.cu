@@ -780,7 +780,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
   }
   if (warp == kWarps && lane == 0) { prefetch_tmap(&mk); prefetch_tmap(&mv); }
   pdl_wait();
-  pdl_trigger();                         // after the wait: the join kernel reads the lengths before its own
+  pdl_trigger();
 
   auto walk = [&] {
     if constexpr (CL) return find_share(a, cs, ips, C::KT, warp == 0);
@@ -1002,12 +1002,12 @@ __device__ __forceinline__ void add_masses(const DecodeArgs& a, const DecodeWs& 
   const int bm = id / chunks, b = bm / a.n_mass, m = bm % a.n_mass;
   const int rows = s.H / a.n_mass, h0 = m * rows;
   const int first = (id % chunks) * TJ * kJoinThreads, step = chunks * TJ * kJoinThreads;
-  const int n = seq_len(a, b);
-  if (first >= n) return;
   float* mass = a.tok_mass + ((size_t)b * a.n_mass + m) * s.L_ctx;
   const double c2d = s.scale * kLog2e;
   const float c2 = (float)c2d;
   pdl_wait();
+  const int n = seq_len(a, b);
+  if (first >= n) return;
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += 64) {
     const int nr = min(64, rows - r0);
@@ -1061,8 +1061,9 @@ __device__ __forceinline__ void add_masses(const DecodeArgs& a, const DecodeWs& 
 // rows), rpc rows each.  Those before them, which take longer: masses, `chunks`
 // CTAs a decision row.
 // Bound by latency: chains of dependent loads, and the first fetch of the
-// code, so loops are short rather than unrolled.  What depends on the lengths
-// alone is done before the wait for the main kernel; each chain's bulk loads
+// code, so loops are short rather than unrolled.  Nothing is read before the wait,
+// the lengths least of all: an append two kernels ahead may have written them, and
+// only the wait orders that write before this grid's reads.  Each chain's bulk loads
 // (partial outputs, logits) are issued ahead of the weights they wait for.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads, 4)
@@ -1081,10 +1082,12 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
     // a warp looks up a row each
     __shared__ Parts s_parts[NW];
     const int row0 = (blockIdx.x - mass_ctas) * rpc, rows = min(rpc, s.batch * s.H - row0);
-    const int n = warp < rows ? seq_len(a, (row0 + warp) / s.H) : 0;
     pdl_wait();
-    if (warp < rows && lane == 0)
-      s_parts[warp] = n > 0 ? parts_of(a, ws, (row0 + warp) / s.H, (row0 + warp) % s.H, rb) : Parts{0, 0, 0};
+    if (warp < rows && lane == 0) {
+      const int b = (row0 + warp) / s.H;
+      const Parts p = parts_of(a, ws, b, (row0 + warp) % s.H, rb);  // of an empty sequence: anything
+      s_parts[warp] = seq_len(a, b) > 0 ? p : Parts{0, 0, 0};
+    }
     __syncthreads();
 #pragma unroll 1
     for (int w = 0; w < rows; ++w) {
