@@ -427,7 +427,10 @@ dl_status dl_qk_norm_rope(const dl_attn_desc* desc, const void* qkv, int64_t qkv
  *   o_h = sum_t e^{a_t - lse} v_t
  * fp32 accumulation, O rounded to nearest-even in the input dtype.  The new
  * token attends to itself when its own key is in the cache (c1 puts it there).
- * L_ctx <= 2^30.  n = 0: O = 0 and lse = -infinity.  A length outside 0..L_ctx counts as 0,
+ * L_ctx <= 2^30.  n = 0: O = 0 and lse = -infinity.  Among the live tokens, a
+ * logit that is NaN makes the row's O, lse and weights NaN, one of +infinity makes
+ * lse +infinity and O and the weights NaN, one of -infinity has no weight (if
+ * all are, O = 0 and lse = -infinity).  A length outside 0..L_ctx counts as 0,
  * and a page slot out of range makes that sequence's results unspecified;
  * both report DL_ERR_BAD_INDEX.
  *   Q        [batch][H][d], O [batch][H][d], 16-byte aligned (desc->L_q == 1)

@@ -219,6 +219,18 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The larger of two, NaN if either is: a NaN dot product has to reach its row's
+// maximum, or a warp that holds nothing else would pass for one without keys.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
 // Two fp32 values as bf16 high parts and bf16 remainders.
 __device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
@@ -328,11 +340,11 @@ struct StateTc {
     float top[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      float t = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      top[r] = fmaxf(m[r], t);
-      raise |= top[r] > m[r];
+      float t = max_nan(max_nan(x[r][0], x[r][1]), max_nan(x[r][2], x[r][3]));
+      t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 1));
+      t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 2));
+      top[r] = max_nan(m[r], t);
+      raise |= !(top[r] <= m[r]);
     }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -516,12 +528,12 @@ struct StateF32 {
       x[r] = ok ? y[0][r] : -INFINITY;
       if (logit && dup == 0 && r < n_rows) logit[(size_t)r * Lp + key] = x[r];
       float t = (float)x[r];
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-      if (NK == 4) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-      top[r] = fmaxf(m[r], t);
-      raise |= top[r] > m[r];
+      t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 1));
+      t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 2));
+      t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 16));
+      if (NK == 4) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 8));
+      top[r] = max_nan(m[r], t);
+      raise |= !(top[r] <= m[r]);
     }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -620,8 +632,10 @@ struct StateF32 {
   }
 };
 
-// Natural log-sum of a row with reference M and sum L (L = 0: no key).
+// Natural log-sum of a row with reference M and sum L (L = 0: no key; a dot product
+// of +infinity makes M that and L NaN).
 __device__ __forceinline__ float lse_of(float M, float L) {
+  if (M == INFINITY) return M;
   return L > 0.0f ? (M + log2f(L)) * kLn2 : (L != L ? L : -INFINITY);
 }
 
@@ -659,7 +673,7 @@ __device__ __forceinline__ void cluster_finish(const DecodeArgs& a, const Decode
     float M = -INFINITY, L = 0.0f;
     float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, ml[k].x);
+    for (int k = 0; k < kMaxCluster; ++k) M = max_nan(M, ml[k].x);
 #pragma unroll
     for (int k = 0; k < kMaxCluster; ++k) {
       const float f = ml[k].x == -INFINITY ? 0.0f : ex2_approx(ml[k].x - M);
@@ -890,7 +904,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     if (lane < RB) {
       float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * RB + lane].x);
+      for (int w = 0; w < kWarps; ++w) M = max_nan(M, s_ml[w * RB + lane].x);
       const float own = s_ml[warp * RB + lane].x;
       s_f[warp][lane] = own == -INFINITY ? 0.0f : ex2_approx(own - M);
     }
@@ -899,7 +913,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     float M = -INFINITY, L = 0.0f;  // row `lane`, on warp 0
     if (warp == 0 && lane < RB) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * RB + lane].x);
+      for (int w = 0; w < kWarps; ++w) M = max_nan(M, s_ml[w * RB + lane].x);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 v = s_ml[w * RB + lane];
@@ -978,13 +992,13 @@ __device__ __forceinline__ float2 row_norm(const DecodeArgs& a, const DecodeWs& 
 #pragma unroll 3
   for (int i = lane; i < p.n; i += 32) {
     const float2 v = ws.pml[(size_t)p.slot(i) * rb + p.r];
-    const float m = fmaxf(M, v.x);
+    const float m = max_nan(M, v.x);
     if (m != -INFINITY) {
       L = L * ex2_approx(M - m) + v.y * ex2_approx(v.x - m);
       M = m;
     }
   }
-  const float top = warp_max(M);
+  const float top = warp_max_nan(M);
   L = warp_sum(top == -INFINITY ? L : L * ex2_approx(M - top));
   return L == 0.0f ? make_float2(INFINITY, 0.0f) : make_float2(top, 1.0f / L);
 }
@@ -1111,12 +1125,12 @@ decode_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__
           for (int q = 0; q < N; ++q) {
             const int i = tid + q * kJoinThreads;
             ml[q] = i < p.n ? ws.pml[(size_t)p.slot(i) * rb + p.r] : make_float2(-INFINITY, 0.0f);
-            M = fmaxf(M, ml[q].x);
+            M = max_nan(M, ml[q].x);
           }
-          M = warp_max(M);
+          M = warp_max_nan(M);
           if (lane == 0) s_m[warp] = M;
           __syncthreads();
-          M = warp_max(s_m[lane % NW]);
+          M = warp_max_nan(s_m[lane % NW]);
 #pragma unroll
           for (int q = 0; q < N; ++q) {
             const int i = tid + q * kJoinThreads;
