@@ -430,7 +430,8 @@ dl_status dl_qk_norm_rope(const dl_attn_desc* desc, const void* qkv, int64_t qkv
  * L_ctx <= 2^30.  n = 0: O = 0 and lse = -infinity.  Among the live tokens, a
  * logit that is NaN makes the row's O, lse and weights NaN, one of +infinity makes
  * lse +infinity and O and the weights NaN, one of -infinity has no weight (if
- * all are, O = 0 and lse = -infinity).  A length outside 0..L_ctx counts as 0,
+ * all are, O = 0 and lse = -infinity); an infinite or NaN value reaches its
+ * column of O, as far as its weight is not below fp32's range.  A length outside 0..L_ctx counts as 0,
  * and a page slot out of range makes that sequence's results unspecified;
  * both report DL_ERR_BAD_INDEX.
  *   Q        [batch][H][d], O [batch][H][d], 16-byte aligned (desc->L_q == 1)

@@ -238,6 +238,14 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint3
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = pack_bf16x2(x - f.x, y - f.y);
 }
+// Two bf16 values, infinities and NaN as the largest finite ones: what the low parts
+// of the weights multiply.  A low part may be 0 or negative, and would turn the
+// infinity that the high part gives into NaN.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
+  asm("min.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0x7F7F7F7Fu));
+  asm("max.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0xFF7FFF7Fu));
+  return v;
+}
 
 template <typename T, int D_, int RB_>
 struct Cfg {
@@ -390,6 +398,8 @@ struct StateTc {
         const uint32_t al[4] = {lo[0][0], lo[1][0], lo[0][1], lo[1][1]};
         mma16816(o[2 * i], ah, vf[0], vf[1]);
         mma16816(o[2 * i + 1], ah, vf[2], vf[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vf[e] = finite_bf16x2(vf[e]);
         mma16816(o[2 * i], al, vf[0], vf[1]);
         mma16816(o[2 * i + 1], al, vf[2], vf[3]);
       }
@@ -404,7 +414,10 @@ struct StateTc {
     }
     if constexpr (NR == 1) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) { o[i][0] += o[i][2]; o[i][1] += o[i][3]; }
+      for (int i = 0; i < D / 8; ++i) {  // beside an infinite value the low sums are NaN: 0 or less times it
+        if (isfinite(o[i][0])) o[i][0] += o[i][2];
+        if (isfinite(o[i][1])) o[i][1] += o[i][3];
+      }
     }
   }
   __device__ __forceinline__ void put_ml(float2* ml, int lane, float c2) const {

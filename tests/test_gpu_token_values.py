@@ -4,6 +4,7 @@ what the formulas give where they define a value, and the documented rest.
   - a NaN dot product: the row's sum is NaN, so O, lse and every weight are;
   - one of +infinity: lse is +infinity, O and the weights are NaN;
   - one of -infinity: weight 0; if every one is, O is 0 and lse -infinity;
+  - an infinite or NaN value reaches its column of O alone.
 Whatever is not named so stays within the bounds of test_gpu_token_step.py."""
 import numpy as np
 import pytest
@@ -11,6 +12,7 @@ import torch
 
 import long_context_diffusion_b200 as dl
 from long_context_diffusion_b200 import pipeline
+from tests.helpers import np_
 from tests.test_gpu_token_step import DT, _cache, _check_decode, _desc, _normal
 
 pytestmark = pytest.mark.gpu
@@ -148,3 +150,31 @@ def test_infinite_dot_products(shape, cuda_device):
     for b in range(B):
         assert torch.isnan(c.O[b, c.heads(0)]).all() and torch.isposinf(c.lse[b, c.heads(0)]).all()
         assert torch.isnan(c.mass[b, 0, :c.lens[b]]).all()
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_infinite_and_nan_values_reach_their_columns(shape, cuda_device):
+    c = Case(shape, 83000)
+    clean = c.V.clone()
+    for b, t in _places(c):
+        slot, row = c.at(b, t)
+        c.V[slot, 1, row, 2], c.V[slot, 1, row, 9] = INF, -INF
+        c.V[slot, 1, row, c.d - 1] = NAN
+    for b in range(B):  # infinities of both signs in one column
+        for t, v in ((0, INF), (c.lens[b] - 1, -INF)):
+            slot, row = c.at(b, t)
+            c.V[slot, 1, row, 17] = v
+    c.run(cuda_device, True)
+    h = c.heads(1)
+    assert torch.isposinf(c.O[:, h, 2]).all() and torch.isneginf(c.O[:, h, 9]).all()
+    assert torch.isnan(c.O[:, h, c.d - 1]).all() and torch.isnan(c.O[:, h, 17]).all()
+    # the other columns, and everything else, as with the clean values
+    c.V = clean
+    keep = [i for i in range(c.d) if i not in (2, 9, 17, c.d - 1)]
+    got = c.O.clone()
+    c.run(cuda_device, True)
+    assert torch.equal(c.O[:, :, keep], got[:, :, keep])
+    for b in range(B):
+        for g in range(H_KV):
+            c.check_kv_head(b, g)
+    assert np.isfinite(np_(got[:, c.heads(0)])).all()
