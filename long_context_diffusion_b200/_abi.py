@@ -269,13 +269,26 @@ def dl_block_scores_noalloc(desc, Q_dec, q_idx, q_cnt, Kbar, n_units, score, str
 CALLS_PATH = os.path.join(_PKG, "lib", "_calls.so")
 
 
-def _load_calls():
-    if not os.path.exists(CALLS_PATH):
-        raise ImportError(
-            f"{CALLS_PATH} is missing: build it with `python -m long_context_diffusion_b200.build`")
-    loader = importlib.machinery.ExtensionFileLoader("_calls", CALLS_PATH)
-    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
-    loader.exec_module(mod)
+class _NoCalls:
+    """In the extension's place where it cannot be used: each call says why.
+    The rest of the library does without it."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name}: {self._why}; build it with `python -m long_context_diffusion_b200.build`")
+
+
+def _load_calls(path: str):
+    if not os.path.exists(path):
+        return _NoCalls(f"{path} is missing")
+    loader = importlib.machinery.ExtensionFileLoader("_calls", path)
+    try:
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+        loader.exec_module(mod)
+    except ImportError as e:  # built for another Python
+        return _NoCalls(f"{path} does not load ({e})")
     return mod
 
 
@@ -286,9 +299,13 @@ def _bind_calls(of):
                   ("dl_qk_norm_rope", "dl_decode_attn", "dl_evict_select", "dl_cache_compact")))
 
 
-_calls = _load_calls()
-if hasattr(torch.Tensor, "__dlpack_c_exchange_api__"):  # else these four calls say what is missing
-    _bind_calls(lib)
+_calls = _load_calls(CALLS_PATH)
+# without the table the extension's calls say what is missing
+if not isinstance(_calls, _NoCalls) and hasattr(torch.Tensor, "__dlpack_c_exchange_api__"):
+    try:
+        _bind_calls(lib)
+    except ImportError as e:  # a table of another version
+        _calls = _NoCalls(str(e))
 
 
 def _raw(stream):

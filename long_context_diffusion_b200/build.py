@@ -52,12 +52,29 @@ def _torch_include() -> str:
     return os.path.join(spec.submodule_search_locations[0], "include")
 
 
-def build_calls() -> str:
-    """The CPython extension of csrc/bind_calls.cpp."""
+def _calls_stamp() -> str:
+    """What a built extension belongs to besides its sources."""
+    import importlib.metadata
+    return "\n".join([sys.version, str(sysconfig.get_config_var("SOABI")), importlib.metadata.version("torch"),
+                      _torch_include()])
+
+
+def build_calls() -> str | None:
+    """The CPython extension of csrc/bind_calls.cpp, built again when a source,
+    Python or torch changed.  None where torch's headers have no exchange table:
+    the library serves its other calls without the extension."""
     src, hdr = os.path.join(CSRC, "bind_calls.cpp"), os.path.join(ROOT, "include", "dl.h")
-    if os.path.exists(CALLS) and os.path.getmtime(CALLS) >= max(os.path.getmtime(src),
-                                                                os.path.getmtime(hdr)):
+    stamp, want = os.path.join(BUILD, "calls.stamp"), _calls_stamp()
+    if os.path.exists(CALLS) and os.path.getmtime(CALLS) >= max(os.path.getmtime(src), os.path.getmtime(hdr)) \
+            and os.path.exists(stamp) and open(stamp).read() == want:
         return CALLS
+    dlpack = os.path.join(_torch_include(), "ATen", "dlpack.h")
+    if not os.path.exists(dlpack) or "DLPackExchangeAPI" not in open(dlpack).read():
+        print(f"{os.path.basename(CALLS)} not built: {dlpack} has no DLPackExchangeAPI; the token-by-token calls are "
+              "not available", file=sys.stderr)
+        if os.path.exists(CALLS):
+            os.remove(CALLS)
+        return None
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I",
            os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"], "-I",
            _torch_include(), src, "-o", CALLS + ".tmp"]
@@ -65,6 +82,8 @@ def build_calls() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(CALLS + ".tmp", CALLS)
+    with open(stamp, "w") as f:
+        f.write(want)
     return CALLS
 
 

@@ -358,4 +358,12 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", "Marshalling of the tok
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls(void) { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__calls(void) {
+  // object layouts differ between minor versions, and nothing in the file's name says which it was built for
+  char built[16];
+  const int n = PyOS_snprintf(built, sizeof(built), "%d.%d.", PY_MAJOR_VERSION, PY_MINOR_VERSION);
+  if (std::strncmp(Py_GetVersion(), built, n) != 0)
+    return PyErr_Format(PyExc_ImportError, "built for Python %d.%d, this is %s", PY_MAJOR_VERSION, PY_MINOR_VERSION,
+                        Py_GetVersion());
+  return PyModule_Create(&g_module);
+}
