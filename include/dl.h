@@ -113,7 +113,9 @@ dl_status dl_get_status(void* stream);
  * (any number of selected blocks or gathered tokens).  The workspace needs
  * 256-byte alignment; its contents need no initialisation and are not
  * preserved between calls.  Calls that share one workspace must be ordered
- * (same stream). */
+ * (same stream).  With L_q 1 this includes dl_decode_attn with masses, whose dot
+ * products take 4 bytes (fp32 keys: 8) per query head and token of capacity;
+ * dl_decode_workspace_size gives what that call alone needs. */
 dl_status dl_workspace_size(const dl_attn_desc* desc, size_t* bytes);
 
 /* (a1) Past-confidence-guided query prediction.  [F2 summary; key point 1]
@@ -448,6 +450,10 @@ dl_status dl_decode_attn(const dl_attn_desc* desc, const void* Q, const void* K_
                          const void* V_pool, const int32_t* page_table, const int32_t* ctx_len,
                          void* O, float* lse, float* tok_mass, int n_mass, float decay, void* ws,
                          size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of a dl_decode_attn call with `desc`, with a tok_mass
+ * (masses != 0) or without one.  Requires what the call does of desc. */
+dl_status dl_decode_workspace_size(const dl_attn_desc* desc, int masses, size_t* bytes);
 
 /* (c3) Which cached tokens leave when a budget is kept.  For each decision
  * row m of a sequence of n = ctx_len[b] tokens with n > budget, `budget`

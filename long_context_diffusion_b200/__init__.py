@@ -13,7 +13,7 @@ from ._abi import (  # noqa: F401
     dl_sink_topn, dl_select,
     dl_block_select, dl_read_counters, key_digit_buffers,
     dl_sparse_attn, dl_token_select, dl_sparse_attn_gather, dl_block_scores_noalloc, LIB_PATH,
-    dl_qk_norm_rope, dl_decode_attn, dl_evict_select, dl_cache_compact,
+    dl_qk_norm_rope, dl_decode_attn, dl_decode_workspace_size, dl_evict_select, dl_cache_compact,
     DL_OK, DL_ERR_INVALID_ARG, DL_ERR_UNSUPPORTED, DL_ERR_WORKSPACE, DL_ERR_CUDA,
     DL_ERR_BAD_INDEX, DL_ERR_TIMEOUT, DL_BF16, DL_FP32,
     DL_FLAG_TOKEN_SIMT, DL_FLAG_GATHER_SIMT, DL_FLAG_PDL, DL_FLAG_SCORE_FP64,

@@ -79,6 +79,8 @@ _SIGS = {
                          _vp, _vp, _vp, _c_int, _vp], _c_int),
     "dl_decode_attn": ([ctypes.POINTER(dl_attn_desc), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                         _c_int, ctypes.c_float, _vp, ctypes.c_size_t, _vp], _c_int),
+    "dl_decode_workspace_size": ([ctypes.POINTER(dl_attn_desc), _c_int,
+                                  ctypes.POINTER(ctypes.c_size_t)], _c_int),
     "dl_evict_select": ([ctypes.POINTER(dl_attn_desc), _vp, _vp, _c_int, _vp, _c_int, _c_int,
                          _c_int, _vp, _vp, _c_int, _vp, _vp, _vp], _c_int),
     "dl_cache_compact": ([ctypes.POINTER(dl_attn_desc), _vp, _vp, _vp, _c_int, _c_int, _vp, _vp,
@@ -336,6 +338,13 @@ def dl_decode_attn(desc, Q, K_pool, V_pool, page_table, ctx_len, O, lse, ws, tok
                             decay, stream if stream is None else _raw(stream))
     if st:
         _check(st)
+
+
+def dl_decode_workspace_size(desc: dl_attn_desc, masses: bool = True) -> int:
+    """Bytes of workspace of a dl_decode_attn call with tok_mass, or without."""
+    n = ctypes.c_size_t(0)
+    _check(lib.dl_decode_workspace_size(ctypes.byref(desc), int(bool(masses)), ctypes.byref(n)))
+    return int(n.value)
 
 
 def dl_evict_select(desc, tok_mass, tok_pos, ctx_len, budget, n_first, n_recent, hole_idx,

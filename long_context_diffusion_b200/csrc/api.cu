@@ -485,16 +485,32 @@ dl_status dl_qk_norm_rope(const dl_attn_desc* desc, const void* qkv, int64_t qkv
   return launched(dl::launch_qk_norm_rope(a, as_stream(stream)), "dl_qk_norm_rope launch");
 }
 
+// The descriptors of dl_decode_attn.
+static dl_status check_decode_desc(const dl_attn_desc* desc, dl::Shape* s, const char* name) {
+  dl_status st = check_desc(desc, s);
+  if (st != DL_OK) return st;
+  if (s->L_q != 1) return fail(DL_ERR_UNSUPPORTED, "%s: L_q=%d (need 1)", name, s->L_q);
+  if (s->L_ctx > dl::kDecodeMaxCtx)
+    return fail(DL_ERR_UNSUPPORTED, "%s: L_ctx=%d (need <= 2^30)", name, s->L_ctx);
+  return DL_OK;
+}
+
+dl_status dl_decode_workspace_size(const dl_attn_desc* desc, int masses, size_t* bytes) {
+  dl::Shape s;
+  dl_status st = check_decode_desc(desc, &s, "dl_decode_workspace_size");
+  if (st != DL_OK) return st;
+  if (!bytes) return fail(DL_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = dl::decode_workspace(s, masses != 0);
+  return ok();
+}
+
 dl_status dl_decode_attn(const dl_attn_desc* desc, const void* Q, const void* K_pool,
                          const void* V_pool, const int32_t* page_table, const int32_t* ctx_len,
                          void* O, float* lse, float* tok_mass, int n_mass, float decay, void* ws,
                          size_t ws_bytes, void* stream) {
   dl::Shape s;
-  dl_status st = check_desc(desc, &s);
+  dl_status st = check_decode_desc(desc, &s, "dl_decode_attn");
   if (st != DL_OK) return st;
-  if (s.L_q != 1) return fail(DL_ERR_UNSUPPORTED, "dl_decode_attn: L_q=%d (need 1)", s.L_q);
-  if (s.L_ctx > dl::kDecodeMaxCtx)
-    return fail(DL_ERR_UNSUPPORTED, "dl_decode_attn: L_ctx=%d (need <= 2^30)", s.L_ctx);
   if (!Q || !K_pool || !V_pool || (!page_table && s.n_pages > 0) || !ctx_len || !O)
     return fail(DL_ERR_INVALID_ARG, "dl_decode_attn: NULL pointer");
   if (!aligned16(Q) || !aligned16(K_pool) || !aligned16(V_pool) || !aligned16(O))

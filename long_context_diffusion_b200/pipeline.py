@@ -314,7 +314,7 @@ class TokenStep:
         self.n_first, self.n_recent, self.decay = n_first, n_recent, decay
         B, H, H_kv, d, L = desc.batch, desc.H, desc.H_kv, desc.d, desc.L_ctx
         n_mass = H_kv if per_head else 1
-        self.ws = workspace(desc, device)
+        self.ws = _empty((A.dl_decode_workspace_size(desc, bool(budget)),), torch.uint8, device)
         self.start = torch.zeros((B,), dtype=torch.int32, device=device)
         self.end = torch.zeros((B,), dtype=torch.int32, device=device)
         self.Q = _empty((B, H, 1, d), dtype, device)
