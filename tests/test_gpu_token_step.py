@@ -89,6 +89,8 @@ ROPE_CASES = [
     ("fp32", 64, 5, 5, 130, 2, 48, True, False, 0),
     ("bf16", 128, 16, 8, 300, 4, 128, True, False, 128),
     # enough tokens for the long-prompt kernel (at least 2 x 148 groups of eight)
+    # -- but of fewer than 1280 values each, which go row by row; with rows enough
+    # for that kernel: the last cases here, and test_gpu_token_prompt.py
     ("bf16", 128, 5, 1, 2373, 1, 128, True, False, 0),
     ("bf16", 64, 4, 2, 1203, 2, 32, True, False, 8),
     ("bf16", 128, 2, 2, 803, 3, 96, False, True, 0),
