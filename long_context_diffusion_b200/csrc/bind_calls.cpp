@@ -218,9 +218,9 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
               x.strides[2] == 1;
   if (fits) {
     n = x.shape[1];
-    // equal steps between all tokens; the strides of single ones say nothing
-    stride = n > 1 ? x.strides[1] : B > 1 ? x.strides[0] : x.shape[2];
-    fits = stride >= x.shape[2] && (B == 1 || n == 1 || x.strides[0] == n * stride);
+    // equal steps between all tokens; the strides of single ones say nothing, and a token alone has none
+    stride = n > 1 ? x.strides[1] : B > 1 ? x.strides[0] : width;
+    fits = (stride >= x.shape[2] || (n == 1 && B == 1)) && (B == 1 || n == 1 || x.strides[0] == n * stride);
   }
   if (!fits) {
     char must[160];

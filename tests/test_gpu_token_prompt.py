@@ -90,3 +90,21 @@ def test_long_prompts_match_the_formula(case, mode, cuda_device):
     for pool in pools:
         assert (np_(pool).transpose(0, 2, 1, 3)[~seen] == 7).all()
     assert np_(end).tolist() == [int(start[b]) + (n if fits[b] else 0) for b in range(B)]
+
+
+@pytest.mark.parametrize("extra", [4, 1, 200])
+def test_a_single_token_may_have_anything_behind_its_heads(extra, cuda_device):
+    """One token has no neighbour, so the width of its tensor is no step."""
+    H, H_kv, d = 4, 2, 64
+    desc = _desc(1, H, H_kv, d, 10, "bf16")
+    x = _normal(98000, 1, 1, (H + 2 * H_kv) * d + extra, dtype=torch.bfloat16)
+    pos = torch.full((1, 1), 77, dtype=torch.int32, device=cuda_device)
+    f = (10000.0 ** (-torch.arange(0, d, 2).double() / d)).float().to(cuda_device)
+    got = []
+    for t in (x, x[..., :(H + 2 * H_kv) * d].contiguous()):
+        o = [torch.full((1, h, 1, d), 9.0, dtype=torch.bfloat16, device=cuda_device) for h in (H, H_kv, H_kv)]
+        dl.dl_qk_norm_rope(desc, t.to(cuda_device), pos, None, None, 0.0, f, *o)
+        got.append(o)
+    assert dl.dl_get_status() == dl.DL_OK
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
