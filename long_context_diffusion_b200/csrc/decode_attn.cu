@@ -3,8 +3,10 @@
 //   a_t = scale q.k_t,  lse = ln sum_t e^{a_t},  o = sum_t e^{a_t - lse} v_t
 //   mass_t <- decay mass_t + sum_h e^{a_t - lse_h}
 //
-// Bound: HBM.  Every key and value row is read once; a KV group of G query
-// heads does 4 G d flops per 4 d bytes (bf16).
+// Bound: HBM.  A key or value row is read once for every block of RB query heads of
+// its KV group: once for groups of up to 16 heads (fp32: 8), ceil(G / RB) times for
+// larger ones, whose blocks are items with copies of their own (4 x 32K, 32/2 heads
+// 31.6 us, 64/2 heads 49.9); a group of G heads does 4 G d flops per 4 d bytes (bf16).
 //
 // Work split.  An item is (sequence, KV head, block of RB query heads); its
 // keys are tiles of KT.  The tiles of all items, in order, are cut into one
@@ -40,7 +42,7 @@
 // of a logit is 1e-6 of its weight, as large as all other errors together.  Groups
 // of up to four heads reach HBM (2 x 32K, 32/8 heads of 128: 5.9 TB/s); with eight
 // (8 x 32K, 32/4 heads) it takes 270 us against 164: issue slots are 54 % busy, the
-// fp64 pipe 24 %, and eight computing warps of 168 registers per SM do not hide the
+// fp64 pipe 24 %, and the eight computing warps (of ten, 168 registers) per SM do not hide the
 // rest (fp32 sums took 215).  Several keys a lane share a read of Q: with one, and
 // quarters of d, 300 us; with Q in registers, every lane four columns and the sums
 // dealt out over 32 lanes, 338.
@@ -78,7 +80,12 @@ constexpr int kMaxCluster = 8;
 // Most tiles of a cluster CTA: 4, or 16 when clusters fill three quarters of the
 // GPU and equal runs would be as long (bf16, d 128, clusters against runs: 8
 // items of 4 tiles a CTA 10.3 to 12.3 us, of 8 tiles 14.4 to 12.3; 32 items of 8
-// tiles 18.3 to 21.4, of 16 tiles 28.1 to 31.2).
+// tiles 18.3 to 21.4, of 16 tiles 28.1 to 31.2).  The same borders serve 64 columns
+// and fp32, back to back in a graph: bf16 of 64, 8 items of 4 tiles 6.8 to 8.3, of 8
+// tiles 9.5 to 8.5; 30 items of 16 tiles 22.0 to 22.3; fp32 of 64, 8 items of 4 tiles
+// 9.1 to 10.1, of 8 tiles 13.8 to 11.0; 30 items of 16 tiles 34.2 to 33.1; fp32 of 128,
+// 8.9 to 9.7, 13.0 to 10.8, 32.4 to 32.0.  Two items of 4 fp32 tiles lose by it (four
+// heads 8.7 to 8.3, eight 11.9 to 10.3), sixty and more win at any size.
 constexpr int kClusterTiles = 4, kClusterTilesFull = 16;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr double kLog2e = 1.4426950408889634;
@@ -96,8 +103,11 @@ __host__ __device__ inline int items_per_seq(const Shape& s) {
 }
 
 // Extra count of an item: at full load a tile takes 1.5 us of a CTA, an item's
-// query load, state join and output 3 to 4 us (ragged 32 x 8K: 0 -> 78 us, 1 ->
-// 70, 3 -> 68, 8 -> 69).
+// query load, state join and output 3 to 4 us (ragged 32 x 8K, 32/8 heads of 128, bf16:
+// 0 -> 64.5 us, 1 -> 60.9, 3 -> 60.4, 6 -> 60.5; of 64: 47.0, 42.6, 40.8, 41.7).  fp32
+// tiles hold as many bytes and take as long or longer, so it serves them too (32/8
+// heads of 64: 80.4, 69.3, 63.5, 66.1; 64/8 of 128: 186, 169, 164, 170; 32 x 2000, 16/8
+// heads of 128: 43.3, 35.6, 30.7, 31.8).
 constexpr int kItemCost = 3;
 
 struct DecodeWs {

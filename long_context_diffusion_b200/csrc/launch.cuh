@@ -19,9 +19,10 @@
 // The token-by-token calls (dl_qk_norm_rope, dl_decode_attn, dl_evict_select,
 // dl_cache_compact) always use it: they run for 4 to 20 us, of which it hides
 // 1.5 to 2 (back to back, eager: norm + rotation of a block 6.2 -> 4.8 us, tiny
-// attention 8.2 -> 6.4, eviction plan 8.9 -> 6.8, 64 moves 6.2 -> 3.9).  In each
-// of their kernels some CTA always reaches pdl_wait(), so that its completion
-// implies its predecessors'.
+// attention 8.2 -> 6.4, eviction plan 8.9 -> 6.8, 64 moves 6.2 -> 3.9).  Every
+// CTA of their kernels reaches pdl_wait(), so that a grid's completion implies its
+// predecessors', and none reads device memory before it: a predecessor that has
+// triggered says nothing of the writes of the kernels before it.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -222,7 +222,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int tiles, int rows_per_
 // and pairs of columns share an instruction (f32x2).  Rows under way stand in a
 // ring of shared memory: asynchronous copies of 16 bytes into slots of the thread
 // that reads them, so that no thread waits for another, across the kinds of heads.
-// 8192 tokens of 96 rows (405 MB): 69.6 us, 5.8 TB/s; 65536: 515 us, 6.3 TB/s.
+// 8192 tokens of 96 rows (405 MB): 70 us, 5.8 TB/s; 65536: 506 us, 6.4 TB/s.
 // With rows loaded ahead into registers 74.5 and 542; two, six and eight rows
 // under way 75.1, 69.9 and 70.2; five CTAs per SM 73.9.
 __device__ __forceinline__ unsigned long long pack2(float x, float y) {
@@ -250,7 +250,7 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigne
 constexpr int kWideTokens = 8, kWideThreads = 128;
 
 // 16 bytes into shared memory.  Of fp32 rows a thread's pieces are halves of a
-// sector, so they pass L1 (139 us at 8192 tokens of 96 rows, 195 beside it).
+// sector, so they pass L1 (133 us at 8192 tokens of 96 rows, 199 beside it).
 template <typename T>
 __device__ __forceinline__ void copy16(uint32_t dst, const T* src) {
   if (sizeof(T) == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -515,9 +515,11 @@ cudaError_t run_rope(const RopeArgs& a, cudaStream_t st) {
   //   tokens 29.8 against 25.0 us, 2400: 30.6 against 31.6, 8192: 69 against 90;
   //   fp32: 2400 tokens 61.4 against 50.6, 3600: 73.5 against 74.8, 8192: 135
   //   against 159);
-  // - a token has the rows to share the coefficients (60000 tokens: 8 rows 78.6
-  //   against 69.3 us, 10: 83.2 against 84.0, 16: 106 against 124; of 64 columns,
-  //   12: 69.9 against 50.7);
+  // - a token has the rows to share the coefficients (60000 tokens: 8 rows 76.0
+  //   against 70.0 us, 10: 82.9 against 83.5, 16: 103 against 120; fp32 99.8 against
+  //   100, 115 against 122, 169 against 190; of 64 columns, 16 rows 73.7 against 63.7,
+  //   20: 80.7 against 76.5, 24: 88.0 against 89.3, 32: 102 against 116; fp32 94.1
+  //   against 83.5, 109 against 103, 126 against 123, 166 against 164);
   // - runs of eight columns are rotated or left alone as a whole.
   if (tt == 8 && !few && all >= (sizeof(T) == 2 ? 2ll : 3ll) * sms && a.rot_dim % 16 == 0) {
     if (a.interleaved)
