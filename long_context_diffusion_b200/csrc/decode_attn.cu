@@ -250,10 +250,10 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint3
 }
 // Two bf16 values, infinities and NaN as the largest finite ones: what the low parts
 // of the weights multiply.  A low part may be 0 or negative, and would turn the
-// infinity that the high part gives into NaN.
+// infinity that the high part gives into NaN.  (8 x 32K, 128/8 heads of 64: 94.0 us,
+// without it 94.5, by a minimum and a maximum 99.4.)
 __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
-  asm("min.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0x7F7F7F7Fu));
-  asm("max.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0xFF7FFF7Fu));
+  asm("min.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0x7F7F7F7Fu));  // v's sign, the smaller magnitude
   return v;
 }
 
