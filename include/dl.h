@@ -382,7 +382,9 @@ dl_status dl_block_scores_noalloc(const dl_attn_desc* desc, const void* Q_dec,
  *     Entries at or behind a sequence's length count for nothing and are not
  *     written.
  *   - These calls do not keep the pooled keys of dl_pool_keys up to date:
- *     call dl_pool_keys before the next block selection over this cache.
+ *     call dl_pool_keys before the next block selection over this cache, or, for
+ *     a denoising step's block, take c1's K_out and V_out and commit them with
+ *     dl_cache_write, which keeps the pooled keys.
  *   - Buffers that a call writes must not overlap any other buffer of the
  *     call, and pages that it writes must belong to one sequence only. */
 

@@ -122,7 +122,7 @@ unsigned kernel_flags() { return g_kernel_flags.load(std::memory_order_relaxed);
 
 extern "C" {
 
-int dl_version(void) { return 300; }
+int dl_version(void) { return 301; }
 
 unsigned dl_set_kernel_flags(unsigned flags) { return g_kernel_flags.exchange(flags); }
 

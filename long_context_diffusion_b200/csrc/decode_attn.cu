@@ -40,7 +40,7 @@
 // S, lane = four columns for O.  The dot products are summed in fp64 and stay so
 // until the reference is subtracted: beside a sink's logit of 35 one fp32 rounding
 // of a logit is 1e-6 of its weight, as large as all other errors together.  Groups
-// of up to four heads reach HBM (2 x 32K, 32/8 heads of 128: 5.9 TB/s); with eight
+// of up to four heads reach HBM (2 x 32K, 32/8 heads of 128: 87 to 99 us from box to box, 5.4 to 6.2 TB/s); with eight
 // (8 x 32K, 32/4 heads) it takes 270 us against 164: issue slots are 54 % busy, the
 // fp64 pipe 24 %, and the eight computing warps (of ten, 168 registers) per SM do not hide the
 // rest (fp32 sums took 215).  Several keys a lane share a read of Q: with one, and
@@ -263,7 +263,7 @@ struct Cfg {
   static constexpr bool BF16 = sizeof(T) == 2;
   // Keys per tile, 32 KB of K and V; half of that for blocks of eight fp32 rows of
   // 64, which 16 keys a warp would spill (32K keys: 357 us against 413; of four
-  // rows 64 keys 179, 32 keys 211).
+  // rows, 8 x 32K, 32/8 heads, 64 keys 184, 32 keys 245).
   static constexpr int KT = BF16 || (D == 64 && RB < 8) ? 64 : 32;
   static constexpr int BOX = KT * 128;                 // bytes of one 128-byte-wide box
   static constexpr int BOXES = D * (int)sizeof(T) / 128;

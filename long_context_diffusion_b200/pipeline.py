@@ -304,6 +304,9 @@ class TokenStep:
     `advance`.  Buffers are allocated once, so a step can be captured in a CUDA
     graph.  `start` holds the cached lengths between steps.
 
+    Pooled keys are not kept (dl_pool_keys refreshes them): a denoising step
+    takes dl_qk_norm_rope's K_out and V_out and commits them with commit_block.
+
     desc: L_q 1, L_ctx the cache's capacity.  budget 0: no masses are kept."""
 
     def __init__(self, desc: A.dl_attn_desc, n_layers: int, dtype: torch.dtype, device, *,

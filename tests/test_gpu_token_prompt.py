@@ -108,3 +108,29 @@ def test_a_single_token_may_have_anything_behind_its_heads(extra, cuda_device):
     assert dl.dl_get_status() == dl.DL_OK
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_a_denoising_block_is_committed_with_its_pooled_keys(cuda_device):
+    """K_out and V_out as a decode block, then dl_cache_write: the rows that an
+    append of the same block writes, with the pooled keys kept."""
+    dev, B, H, H_kv, d, n, L = cuda_device, 2, 8, 4, 128, 32, 192
+    desc = _desc(B, H, H_kv, d, L, "bf16")
+    table = _table(98500, B, desc.n_pages, desc.n_slots).to(dev)
+    x = _normal(98501, B, n, (H + 2 * H_kv) * d, dtype=torch.bfloat16).to(dev)
+    pos = (torch.arange(n, dtype=torch.int32, device=dev) + 100).expand(B, n).contiguous()
+    f = (10000.0 ** (-torch.arange(0, d, 2).double() / d)).float().to(dev)
+    w = torch.ones(d, dtype=torch.bfloat16, device=dev)
+    start = torch.tensor([100, 7], dtype=torch.int32, device=dev)
+    pools = [[_normal(98502 + j, desc.n_slots, H_kv, 64, d, dtype=torch.bfloat16).to(dev) for j in range(2)] for _ in range(2)]
+    Q = torch.empty(B, H, n, d, dtype=torch.bfloat16, device=dev)
+    dl.dl_qk_norm_rope(desc, x, pos, w, w, 1e-6, f, Q, start=start, page_table=table, K_pool=pools[0][0], V_pool=pools[0][1])
+    K, V = (torch.empty(B, H_kv, n, d, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    kbar, want = (torch.empty(B, H_kv, desc.n_pages, d, device=dev) for _ in range(2))
+    dl.dl_pool_keys(desc, pools[1][0], table, desc.n_pages, 64, 0, 64, kbar)
+    dl.dl_qk_norm_rope(desc, x, pos, w, w, 1e-6, f, Q, K, V)
+    dl.dl_cache_write(desc, K, V, start, table, *pools[1], kbar)
+    dl.dl_pool_keys(desc, pools[0][0], table, desc.n_pages, 64, 0, 64, want)
+    assert dl.dl_get_status() == dl.DL_OK
+    for a, b in zip(pools[0], pools[1]):
+        assert torch.equal(a, b)
+    assert torch.equal(kbar, want)
