@@ -400,8 +400,9 @@ dl_status dl_block_scores_noalloc(const dl_attn_desc* desc, const void* Q_dec,
  *   for j < rot_dim/2, with a = p * inv_freq[j]:
  *     (y_u, y_v) <- (y_u cos a - y_v sin a, y_v cos a + y_u sin a),
  *     (u, v) = (j, j + rot_dim/2), or (2j, 2j+1) when interleaved != 0;
- * values are only copied.  Computed in fp32 (the angle and its reduction in
- * fp64, so that far positions keep their phase), rounded once to the dtype.
+ * values are only copied.  Computed in fp32, the sum of squares included (a row
+ * with values beyond about 1e18 is outside its range; the angle and its reduction
+ * in fp64, so that far positions keep their phase), rounded once to the dtype.
  *   pos       int32 [batch][n_tok], any value
  *   inv_freq  fp32 [rot_dim/2] (NULL when rot_dim is 0); rot_dim a multiple
  *             of 8, 0..d

@@ -54,9 +54,10 @@ def _torch_include() -> str:
 
 def _calls_stamp() -> str:
     """What a built extension belongs to besides its sources."""
-    import importlib.metadata
-    return "\n".join([sys.version, str(sysconfig.get_config_var("SOABI")), importlib.metadata.version("torch"),
-                      _torch_include()])
+    include = _torch_include()
+    version = os.path.join(os.path.dirname(include), "version.py")
+    return "\n".join([sys.version, str(sysconfig.get_config_var("SOABI")), include,
+                      open(version).read() if os.path.exists(version) else ""])
 
 
 def build_calls() -> str | None:
@@ -75,6 +76,7 @@ def build_calls() -> str | None:
         if os.path.exists(CALLS):
             os.remove(CALLS)
         return None
+    os.makedirs(BUILD, exist_ok=True)
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I",
            os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"], "-I",
            _torch_include(), src, "-o", CALLS + ".tmp"]

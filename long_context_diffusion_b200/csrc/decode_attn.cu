@@ -40,12 +40,12 @@
 // S, lane = four columns for O.  The dot products are summed in fp64 and stay so
 // until the reference is subtracted: beside a sink's logit of 35 one fp32 rounding
 // of a logit is 1e-6 of its weight, as large as all other errors together.  Groups
-// of up to four heads reach HBM (2 x 32K, 32/8 heads of 128: 87 to 99 us from box to box, 5.4 to 6.2 TB/s); with eight
-// (8 x 32K, 32/4 heads) it takes 270 us against 164: issue slots are 54 % busy, the
-// fp64 pipe 24 %, and the eight computing warps (of ten, 168 registers) per SM do not hide the
-// rest (fp32 sums took 215).  Several keys a lane share a read of Q: with one, and
-// quarters of d, 300 us; with Q in registers, every lane four columns and the sums
-// dealt out over 32 lanes, 338.
+// of up to four heads reach HBM (2 x 32K, 32/8 heads of 128: 87 to 99 us from card to
+// card, 5.4 to 6.2 TB/s); with eight (8 x 32K, 32/4 heads) it takes 270 us against 164:
+// issue slots are 54 % busy, the fp64 pipe 24 %, and the eight computing warps (of ten,
+// 168 registers) per SM do not hide the rest (fp32 sums took 215).  Several keys a lane
+// share a read of Q: with one, and quarters of d, 300 us; with Q in registers, every
+// lane four columns and the sums dealt out over 32 lanes, 338.
 //
 // Weights.  With c = scale log2 e and a maximum m of the dot products x, the
 // reference is M = m c rounded once, and p = 2^(x c - M) in one fused

@@ -117,3 +117,29 @@ assert torch.allclose(step.lse[0].exp(), torch.full_like(step.lse[0], 200.0) + t
 def test_the_first_calls_of_a_process_may_be_captured(cuda_device):
     r = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("L,lens", [(100, [100]), (3300, [3201])])
+def test_thousands_of_heads_of_one_group(dtype, L, lens, cuda_device):
+    H, d, dt = 2500, 64, DT[dtype]
+    K, V, table = _cache(103000 + L, 1, 1, d, lens, L, dt)
+    desc = _desc(1, H, 1, d, L, dtype, n_slots=K.shape[0])
+    Q = _normal(103990 + L, 1, H, d, dtype=dt)
+    mass0 = torch.full((1, 1, L), 0.5)
+    put = lambda t: t.to(cuda_device)  # noqa: E731
+    mass = put(mass0)
+    O, lse = torch.empty(1, H, d, dtype=dt, device=cuda_device), torch.empty(1, H, device=cuda_device)
+    dl.dl_decode_attn(desc, put(Q), put(K), put(V), put(table), put(torch.tensor(lens, dtype=torch.int32)), O, lse,
+                      pipeline.workspace(desc, cuda_device), tok_mass=mass, decay=0.5)
+    assert dl.dl_get_status() == dl.DL_OK
+    # a mass adds 2500 weights in turn: one rounding each of the sum so far, beside the weights' own
+    n = lens[0]
+    m = mass[0, 0, :n].double().cpu() - 0.25
+    _check_decode(Q, K, V, table, lens, O, lse, None, None, 0.5, dtype, 1, 0)
+    k = K[table[0].long()].reshape(-1, d)[:n].double()
+    w = torch.softmax(Q[0].double() @ k.T / d ** 0.5, 1).sum(0)
+    delta = (2 * d + 8) * U * float(Q.double().norm(dim=-1).max() * k.norm(dim=1).max()) / d ** 0.5
+    eps_w = 2 * delta + (n + 64) * U + (2.0 ** -16 if dtype == "bf16" else 0.0)
+    assert ((m - w).abs() <= 2 * eps_w * w + (H + 4) * U * (w + 0.25)).all()
+    assert (mass[0, 0, n:] == 0.5).all()

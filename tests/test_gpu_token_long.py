@@ -4,14 +4,12 @@ replayed with growing lengths and run without gaps; masses that all heads of a
 sequence share, on clusters and on runs.
 
 Tolerances: those of test_gpu_token_step.py."""
-import numpy as np
 import pytest
 import torch
 
 import long_context_diffusion_b200 as dl
-import synth
 from long_context_diffusion_b200 import pipeline
-from tests.test_gpu_token_step import DT, SEED, _cache, _check_decode, _desc, _normal, _table
+from tests.test_gpu_token_step import DT, _busy_run, _check_decode, _desc, _normal, _table
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +128,11 @@ def test_captured_long_step_replays_with_growing_lengths(case, cuda_device):
         mass0[1][b, :, lens[b] - 1] = 0  # what the append leaves
     _check_decode(step.Q[:, :, 0].cpu(), pools[1][0].cpu(), pools[1][1].cpu(), table.cpu(), lens, step.O[1], step.lse[1],
                   mass0[1], step.tok_mass[1], 0.5, dtype, H_kv, step.tok_mass[1].shape[1])
+
+
+def test_calls_without_gaps_behind_programmatic_launches_of_the_framework(kernel_flags, cuda_device):
+    """The same with the framework's other kernels launched programmatically too."""
+    want = _busy_run(cuda_device, True)
+    kernel_flags(dl.DL_FLAG_PDL)
+    for a, b in zip(_busy_run(cuda_device, False), want):
+        assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
